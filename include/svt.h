@@ -5,7 +5,7 @@
  *
  * Common rules for every entry point below
  * ----------------------------------------
- *  - Every array argument is a DEVICE pointer owned by the caller (cudaMalloc, a PyTorch
+ *  - Every array argument (but that of svt_rope_frequencies) is a DEVICE pointer owned by the caller (cudaMalloc, a PyTorch
  *    tensor, ...). The library never allocates device memory, never frees what it is given
  *    and never synchronises the stream (except svt_read_status, whose job is to read back).
  *  - Every call is asynchronous on `stream` (a cudaStream_t; NULL = the legacy default stream)
@@ -294,6 +294,140 @@ SVT_API svt_status svt_merge_splits(const float* o_part, const float* lse_part, 
  */
 SVT_API svt_status svt_topk_select(const float* scores, int32_t T, int32_t N, int64_t stride, const int32_t* lens,
                                    int32_t K, int32_t* topk_out, svt_stream_t stream);
+
+/*
+ * Rotary positions. A pair (a, b) of rotated columns of a token at position pos becomes
+ *   a' = amplitude * (a cos - b sin),  b' = amplitude * (a sin + b cos),  angle = pos * freqs[pair]
+ * over the dim columns that start at `offset` of each row of D columns; the other columns are
+ * copied (left alone when out is x). Any rule for long contexts is a choice of frequencies and
+ * amplitude: svt_rope_frequencies writes the usual ones.
+ */
+typedef enum { SVT_BF16 = 0, SVT_F32 = 1 } svt_dtype;
+typedef enum {
+  SVT_ROPE_INTERLEAVED = 0, /* pair i = columns 2 i and 2 i + 1        */
+  SVT_ROPE_HALF = 1         /* pair i = columns i and i + dim / 2      */
+} svt_rope_layout;
+typedef enum {
+  SVT_ROPE_SCALE_NONE = 0,
+  SVT_ROPE_SCALE_LINEAR = 1,       /* every frequency / factor                                       */
+  SVT_ROPE_SCALE_BY_PARTS = 2,     /* by pair index: pairs that make at least `fast` turns over
+                                      original_len keep their frequency, those that make at most
+                                      `slow` are divided by factor, a linear ramp over the pair index
+                                      (bounds rounded outwards) lies between                          */
+  SVT_ROPE_SCALE_BY_WAVELENGTH = 3 /* the same bands with the ramp linear in the number of turns      */
+} svt_rope_scale_kind;
+typedef struct {
+  svt_rope_scale_kind kind;
+  double factor;        /* > 0                                         */
+  double original_len;  /* tokens the unscaled frequencies were made for */
+  double fast, slow;    /* turns over original_len, fast > slow > 0    */
+} svt_rope_scaling;
+
+/* Writes dim / 2 frequencies (radians per position, base^(-2 i / dim), scaled) to the HOST array
+ * freqs. dim even, 2 .. 512; scaling NULL = none. The one call here that takes a host array:
+ * copy it to the device once and keep it. */
+SVT_API svt_status svt_rope_frequencies(int32_t dim, double base, const svt_rope_scaling* scaling, double* freqs);
+
+/*
+ *   x, out        [T, H, D] rows of D contiguous elements at element strides (t, h), any alignment of
+ *                 whole elements (rows and columns that split into 16-byte units are faster). out may
+ *                 be x (same strides); otherwise they must not overlap. Rows of out must not overlap.
+ *   positions     [T] int32, any value. Angles are reduced modulo a turn in 64-bit fixed point before
+ *                 they are rounded to fp32: far positions are as exact as an fp64 product.
+ *   freqs         [dim / 2] fp64 device array, radians per position. dim even, at most 512.
+ *   inverse       non-zero: the angles negated. With the same amplitude this is the transpose, which
+ *                 maps the gradient of out to the gradient of x.
+ * Arithmetic in fp32, rounded once to dtype. H and D at most 16384, T * H < 2^31. One kernel, no
+ * workspace.
+ */
+SVT_API svt_status svt_rope(const void* x, void* out, svt_dtype dtype, int32_t T, int32_t H, int32_t D,
+                            int64_t x_stride_t, int64_t x_stride_h, int64_t out_stride_t, int64_t out_stride_h,
+                            const int32_t* positions, const double* freqs, int32_t dim, int32_t offset,
+                            svt_rope_layout layout, float amplitude, int32_t inverse, svt_stream_t stream);
+
+/*
+ * Writes new cache rows: token t's latent columns and its rotated rope columns go to cache row
+ * slots[t], in the layouts of svt_kv_cache. The same launch can rotate the tokens' query heads.
+ *   latent        [T, 512] bf16, rows at latent_stride elements and on 16-byte boundaries.
+ *   k_rope        [T, 64] bf16 before rotation, rows at k_rope_stride elements.
+ *   positions     [T] int32. slots [T] int32: a negative slot writes nothing; one at or past the
+ *                 cache's rows writes nothing and sets SVT_DEV_ERR_INDEX_RANGE. Slots must be distinct:
+ *                 a row named by two tokens ends up with columns of either.
+ *   kv            the cache that is written (either dtype); rows no slot names are left as they were.
+ *                 e4m3: each block of 128 channels gets scale = largest magnitude / 448 (1 for a block
+ *                 of zeros) and the codes nearest to value / scale, in IEEE fp32 division. A latent
+ *                 value beyond 65504 (or NaN) or a rotated one the f16 arithmetic of that cache cannot
+ *                 hold sets SVT_DEV_ERR_FP8_RANGE; the row is written all the same.
+ *   freqs         [32] fp64 device array; layout and amplitude as for svt_rope.
+ *   q_rope, q_out [T, H, 64] bf16 at element strides (t, h): the queries' rope columns, rotated from
+ *                 q_rope into q_out (for instance columns 512 .. 575 of q). Both NULL: no queries.
+ * Workspace: the 256-byte status header. One kernel.
+ */
+SVT_API svt_status svt_rope_append(const void* latent_bf16, int64_t latent_stride, const void* k_rope_bf16,
+                                   int64_t k_rope_stride, const int32_t* positions, const int32_t* slots, int32_t T,
+                                   const svt_kv_cache* kv, const double* freqs, svt_rope_layout layout,
+                                   float amplitude, const void* q_rope_bf16, int32_t H, int64_t q_stride_t,
+                                   int64_t q_stride_h, void* q_out_bf16, int64_t q_out_stride_t,
+                                   int64_t q_out_stride_h, void* ws, size_t ws_bytes, svt_stream_t stream);
+
+/*
+ * The backward pass of svt_sparse_mla_decode (and of a grouped prefill: each query's own list), with
+ * the probabilities recomputed from q, the cache and lse:
+ *   P = exp(scale q K^T - lse),  delta = sum_c dout out - dlse,  dS = P (dout V^T - delta) scale,
+ *   dq = dS K,   gradient of a cache row = the sum of dS^T q + P^T dout over the lists that hold it.
+ *   q, kv, block_table .. topk_len, softmax_scale  as for svt_sparse_mla_decode; a bf16 cache only
+ *                 (SVT_ERR_UNSUPPORTED otherwise: the codes of an e4m3 cache are not differentiable).
+ *                 A request id, position or slot out of range is dead and sets
+ *                 SVT_DEV_ERR_INDEX_RANGE. An entry listed twice counts twice, as in the forward.
+ *   out, lse      the forward's [T, H, 512] bf16 and [T, H] fp32. A row with lse = -inf (no live
+ *                 entry) has no gradient.
+ *   dout, dlse    gradients of out ([T, H, 512] bf16) and of lse ([T, H] fp32, NULL = zero).
+ *   dq            [T, H, 576] bf16.
+ *   dkv           [num_pages * page_size, 576] bf16, packed: written whole, zero where no list reaches.
+ *   weights       [T, K] fp32 or NULL: each entry's probability summed over the heads (0 for a dead
+ *                 entry): what an eviction rule accumulates, or the teacher of svt_distill_topk.
+ * P and dS are rounded to bf16 once, as operands of the tensor cores; every sum is fp32. Cache rows'
+ * sums are fp32 atomic additions: their order, and so the last bits of dkv, may differ between calls.
+ * Workspace: svt_sparse_mla_backward_workspace_size(T, H, K, num_pages * page_size); the call leaves
+ * its contents behind the status header undefined and needs none of them zero.
+ */
+SVT_API size_t svt_sparse_mla_backward_workspace_size(int32_t T, int32_t H, int32_t K, int64_t num_slots);
+SVT_API svt_status svt_sparse_mla_backward(const void* q_bf16, int32_t T, int32_t H, const svt_kv_cache* kv,
+                                           const int32_t* block_table, int32_t num_reqs, int32_t max_blocks,
+                                           const int32_t* req_of_token, const int32_t* seq_lens, const int32_t* topk,
+                                           int32_t K, const int32_t* topk_len, float softmax_scale,
+                                           const void* out_bf16, const float* lse, const void* dout_bf16,
+                                           const float* dlse, void* dq_bf16, void* dkv_bf16, float* weights, void* ws,
+                                           size_t ws_bytes, svt_stream_t stream);
+
+/*
+ * The loss that trains an indexer's scores (what svt_topk_select selects from) on a teacher's top
+ * entries, and its gradient. Per query t, over the live entries j of its list:
+ *   p = the teacher's values normalised to sum 1 (SVT_TEACHER_WEIGHTS, values >= 0), or
+ *       softmax(values / temperature) (SVT_TEACHER_LOGITS);
+ *   q = softmax(scores / temperature) over positions 0 .. len - 1 (SVT_DISTILL_CANDIDATES), or over
+ *       the live entries (SVT_DISTILL_LISTED);
+ *   loss[t] = sum_j p_j (ln p_j - ln q_j),
+ *   dscores[t, n] = row_weight[t] / temperature * (q_n - p_n), 0 outside the softmax's range.
+ *   scores        [T, N] fp32 or bf16, row t starting at scores + t * stride elements.
+ *   lens          [T] int32 candidates per query, clamped to [0, N]; NULL = N.
+ *   topk, teacher [T, K] int32 positions and fp32 values, packed, in any order; an entry outside
+ *                 [0, len) is dead. A position listed twice counts twice. K >= 1.
+ *   temperature   1e-6 .. 1e6 (weights are not changed by it).
+ *   row_weight    [T] fp32, or NULL for 1: the gradient that arrives at loss[t].
+ *   loss          [T] fp32 or NULL. dscores [T, N] like scores, at dstride, or NULL; it must not
+ *                 overlap scores; all N columns are written.
+ * A query whose teacher values are all 0 (or which has no live entry), or whose scores are all -inf,
+ * has loss 0 and gradient 0. A listed score of -inf among others gives an infinite loss; NaN inputs
+ * give NaN in their own row alone. One kernel, no workspace.
+ */
+typedef enum { SVT_TEACHER_WEIGHTS = 0, SVT_TEACHER_LOGITS = 1 } svt_teacher_kind;
+typedef enum { SVT_DISTILL_CANDIDATES = 0, SVT_DISTILL_LISTED = 1 } svt_distill_scope;
+SVT_API svt_status svt_distill_topk(const void* scores, svt_dtype dtype, int32_t T, int32_t N, int64_t stride,
+                                    const int32_t* lens, const int32_t* topk, const float* teacher, int32_t K,
+                                    svt_teacher_kind kind, svt_distill_scope scope, float temperature,
+                                    const float* row_weight, float* loss, void* dscores, int64_t dstride,
+                                    svt_stream_t stream);
 
 /*
  * Gather probe, a measurement tool rather than a step of the method: reads the cache rows of

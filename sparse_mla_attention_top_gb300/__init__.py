@@ -14,9 +14,14 @@ from .svt import (  # noqa: F401
     Workspace,
     build_group_union,
     debug_pipeline_fault,
+    distill_topk,
     gather_probe,
     merge_splits,
     resolve_topk_slots,
+    rope,
+    rope_append,
+    rope_frequencies,
+    sparse_mla_backward,
     sparse_mla_decode,
     sparse_mla_prefill_grouped,
     tensor_probe,

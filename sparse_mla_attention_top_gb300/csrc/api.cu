@@ -194,6 +194,9 @@ void debug_fault_state(int* fault, unsigned long long* wait_limit_ns) {
   *wait_limit_ns = g_debug_wait_limit_ns.load(std::memory_order_relaxed);
 }
 
+svt_status check_kv_cache(const svt_kv_cache* kv, long long* row_stride) { return check_kv(kv, row_stride); }
+svt_status check_workspace(void* ws, size_t ws_bytes, size_t need) { return check_ws(ws, ws_bytes, need); }
+
 svt_status set_last_error(svt_status st, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);

@@ -193,6 +193,85 @@ int pair_prefill_clusters();
 // right behind the attention kernel (programmatic dependent launch) and waiting for it.
 cudaError_t launch_streamk_merge(const AttnParams& p, cudaStream_t stream);
 
+// Rotation of rows [T, H] of D columns (strides in elements): columns offset .. offset + dim - 1
+// are turned, the others copied when out is not x. The launcher fills the fields after `sign`.
+struct RopeParams {
+  const void* x;
+  void* out;
+  int T, H, D, dim, offset;
+  long long x_stride_t, x_stride_h, out_stride_t, out_stride_h;
+  const int32_t* positions;  // [T]
+  const double* freqs;       // [dim / 2] radians per position
+  float amplitude, sign;     // sign: 1, or -1 for the transposed rotation
+  int units, rot_units, rows_per_cta;
+  uint32_t magic_units, magic_h;
+};
+cudaError_t launch_rope(const RopeParams& p, bool f32, bool half, cudaStream_t stream);
+
+// New cache rows from latent [T, 512] and unrotated k_rope [T, 64] (bf16, strides in elements).
+struct AppendParams {
+  const uint16_t* latent;
+  long long latent_stride;
+  const uint16_t* k_rope;
+  long long k_rope_stride;
+  const int32_t* positions;
+  const int32_t* slots;
+  const double* freqs;
+  float amplitude;
+  uint8_t* kv;
+  long long row_stride, num_slots;
+  int T;
+  int* status;
+  int row_ctas;  // filled by the launcher
+};
+// rope.H = 0: rows only.
+cudaError_t launch_append(const AppendParams& p, const RopeParams& rope, bool f8, bool half, cudaStream_t stream);
+
+// The top-entry distillation loss and its gradient (strides in elements; loss, dscores, lens and
+// row_weight may be null). The launcher fills split.
+struct DistillParams {
+  const void* scores;
+  long long stride;
+  const int32_t* lens;
+  const int32_t* idx;
+  const float* teacher;
+  int T, N, K;
+  bool logits;
+  float inv_tau;
+  const float* row_weight;
+  float* loss;
+  void* dscores;
+  long long dstride;
+  int vec;  // rows of scores and dscores start on 16-byte boundaries
+  int split;
+};
+cudaError_t launch_distill(const DistillParams& p, bool f32, bool all, cudaStream_t stream);
+
+// The attention's backward pass.
+struct BackwardParams {
+  const uint16_t* q;     // [T, H, 576]
+  const uint16_t* out;   // [T, H, 512]
+  const uint16_t* dout;  // [T, H, 512]
+  const float* lse;      // [T, H]
+  const float* dlse;     // [T, H] or null
+  const uint8_t* kv;
+  long long row_stride, num_slots;
+  int T, H, K;
+  float scale;
+  const int32_t* slots;  // [T, K] resolved, -1 = dead
+  uint16_t* dq;          // [T, H, 576]
+  uint16_t* dkv;         // [num_slots, 576]
+  float* weights;        // [T, K] or null
+  float* dkv_acc;        // [num_slots, 576], zero on entry
+  float* dq_acc;         // [T, H, 576], zero on entry
+  int* status;
+};
+cudaError_t launch_backward(const BackwardParams& p, cudaStream_t stream);
+
+// The checks of a cache descriptor (and its row stride) and of a workspace that every entry point makes.
+svt_status check_kv_cache(const svt_kv_cache* kv, long long* row_stride);
+svt_status check_workspace(void* ws, size_t ws_bytes, size_t need);
+
 // svt_sparse_mla_decode with one more option: after every argument check has passed and
 // before the kernels, clear the workspace's status word (clear_status_first).
 svt_status sparse_mla_decode_enqueue(const void* q_bf16, int32_t T, int32_t H, const svt_kv_cache* kv,

@@ -26,6 +26,10 @@ DEV_ERR_TIMEOUT = 0x2
 DEV_ERR_FP8_RANGE = 0x4
 KV_BF16 = 0
 KV_FP8_E4M3 = 1
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "by_parts": 2, "by_wavelength": 3}
+TEACHER_KINDS = {"weights": 0, "logits": 1}
+DISTILL_SCOPES = {"candidates": 0, "listed": 1}
 ROW_BYTES = {KV_BF16: 1152, KV_FP8_E4M3: 656}
 
 EXPORTED = [
@@ -35,6 +39,8 @@ EXPORTED = [
     "svt_sparse_mla_prefill_grouped_workspace_size", "svt_sparse_mla_prefill_grouped",
     "svt_sparse_mla_prefill_grouped_union_tile", "svt_merge_splits",
     "svt_topk_select",
+    "svt_rope_frequencies", "svt_rope", "svt_rope_append", "svt_sparse_mla_backward_workspace_size",
+    "svt_sparse_mla_backward", "svt_distill_topk",
     "svt_sparse_mla_decode_noalloc", "svt_debug_pipeline_fault", "svt_gather_probe", "svt_tensor_probe",
 ]
 
@@ -48,6 +54,11 @@ class SvtError(RuntimeError):
 class _KV(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
                 ("row_stride_bytes", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double), ("original_len", ctypes.c_double),
+                ("fast", ctypes.c_double), ("slow", ctypes.c_double)]
 
 
 def library_path() -> Path:
@@ -90,6 +101,15 @@ def lib():
         L.svt_sparse_mla_prefill_grouped_union_tile.argtypes = L.svt_sparse_mla_prefill_grouped.argtypes
         L.svt_merge_splits.argtypes = [P, P, i32, i32, i32, P, P, P]
         L.svt_topk_select.argtypes = [P, i32, i32, i64, P, i32, P, P]
+        L.svt_rope_frequencies.argtypes = [i32, ctypes.c_double, ctypes.POINTER(_RopeScaling), P]
+        L.svt_rope.argtypes = [P, P, i32, i32, i32, i32, i64, i64, i64, i64, P, P, i32, i32, i32, f32, i32, P]
+        L.svt_rope_append.argtypes = [P, i64, P, i64, P, P, i32, ctypes.POINTER(_KV), P, i32, f32, P, i32, i64, i64, P,
+                                      i64, i64, P, sz, P]
+        L.svt_sparse_mla_backward_workspace_size.argtypes = [i32, i32, i32, i64]
+        L.svt_sparse_mla_backward_workspace_size.restype = sz
+        L.svt_sparse_mla_backward.argtypes = [P, i32, i32, ctypes.POINTER(_KV), P, i32, i32, P, P, P, i32, P, f32, P, P,
+                                              P, P, P, P, P, P, sz, P]
+        L.svt_distill_topk.argtypes = [P, i32, i32, i32, i64, P, P, P, i32, i32, i32, f32, P, P, P, i64, P]
         L.svt_sparse_mla_decode_noalloc.argtypes = [P, i32, i32, ctypes.POINTER(_KV), P, i32, i32, P, P, P, i32, P, f32,
                                                     P, P, i32, P, P]
         L.svt_debug_pipeline_fault.argtypes = [i32, i64]
@@ -290,6 +310,206 @@ def topk_select(scores, K: int, *, lens=None, out=None):
     _check(lib().svt_topk_select(_ptr(scores), T, N, stride, _ptr(lens), int(K), _ptr(out), _stream()),
            "svt_topk_select")
     return out
+
+
+def _on_device(device, **tensors) -> None:
+    """Every given tensor is on `device`, which is the current CUDA device (kernels are launched
+    there, on its current stream)."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise TypeError(f"tensors must be on the current CUDA device, not {device}")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise TypeError(f"{name} must be on {device}, not {t.device}")
+
+
+def _shaped(t, name: str, dtype, shape):
+    """`t`, when it is None or a contiguous tensor of this type and shape."""
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    return t
+
+
+def _choice(value: str, choices: dict, name: str) -> int:
+    if value not in choices:
+        raise ValueError(f"{name} must be one of {', '.join(choices)}, got {value!r}")
+    return choices[value]
+
+
+def _rows3(x, name: str):
+    """x [T, D] or [T, H, D] as (T, H, D, stride t, stride h); unit column stride. A dimension of
+    one row has no meaningful stride."""
+    if x.dim() not in (2, 3) or (x.shape[-1] > 1 and x.stride(-1) != 1):
+        raise TypeError(f"{name} must be [T, D] or [T, H, D] with unit column stride")
+    T, H, D = (x.shape[0], 1, x.shape[1]) if x.dim() == 2 else x.shape
+    sh = D if x.dim() == 2 or H <= 1 else x.stride(1)
+    st = H * D if T <= 1 else x.stride(0)
+    return T, H, D, st, sh
+
+
+def rope_frequencies(dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+                     original_len: float = 0.0, fast: float = 32.0, slow: float = 1.0, device=None):
+    """svt_rope_frequencies: the [dim / 2] fp64 frequencies (radians per position) that rope and
+    rope_append take, on the device. scaling: "none", "linear", "by_parts" or "by_wavelength"."""
+    host = torch.empty(max(0, int(dim) // 2), dtype=torch.float64)
+    s = _RopeScaling(_choice(scaling, ROPE_SCALINGS, "scaling"), float(factor), float(original_len), float(fast),
+                     float(slow))
+    _check(lib().svt_rope_frequencies(int(dim), float(base), ctypes.byref(s), _ptr(host)), "svt_rope_frequencies")
+    return host.to(torch.device("cuda", torch.cuda.current_device()) if device is None else device)
+
+
+def _freqs(freqs):
+    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise TypeError("freqs must be a contiguous fp64 [dim / 2] tensor")
+    return freqs
+
+
+def rope(x, positions, freqs, *, offset: int = 0, layout: str = "interleaved", inverse: bool = False,
+         amplitude: float = 1.0, out=None):
+    """svt_rope: rotates columns offset .. offset + 2 len(freqs) - 1 of x ([T, H, D] or [T, D], bf16
+    or fp32, rows may be strided) by its tokens' positions; the other columns are copied. out=x
+    rotates in place. inverse=True turns back: it maps the gradient of the result to x's."""
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("x must be bf16 or fp32")
+    T, H, D, xt, xh = _rows3(x, "x")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if out.dtype != x.dtype or out.shape != x.shape:
+        raise TypeError("out must have x's type and shape")
+    _, _, _, ot, oh = _rows3(out, "out")
+    dim = 2 * _freqs(freqs).numel()
+    _shaped(_i32(positions, "positions"), "positions", torch.int32, (T,))
+    _on_device(x.device, positions=positions, freqs=freqs, out=out)
+    _check(lib().svt_rope(_ptr(x), _ptr(out), 1 if x.dtype == torch.float32 else 0, T, H, D, xt, xh, ot, oh,
+                          _ptr(positions), _ptr(freqs), dim, int(offset), _choice(layout, ROPE_LAYOUTS, "layout"),
+                          float(amplitude), int(bool(inverse)), _stream()), "svt_rope")
+    return out
+
+
+def rope_append(latent, k_rope, positions, slots, kv: KVCache, freqs, *, layout: str = "interleaved",
+                amplitude: float = 1.0, q_rope=None, q_out=None, ws: Optional[Workspace] = None):
+    """svt_rope_append: writes latent [T, 512] and the rotated k_rope [T, 64] (bf16, rows may be
+    strided) to cache rows slots [T] (negative: skipped); with q_rope [T, H, 64] it rotates the
+    queries' rope columns into q_out (a new tensor when None; q[..., 512:] of a [T, H, 576] q fits)
+    in the same launch. Returns q_out."""
+    for name, t, width in (("latent", latent, 512), ("k_rope", k_rope, 64)):
+        if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1:
+            raise TypeError(f"{name} must be a bf16 [T, {width}] tensor with unit column stride")
+    T = latent.shape[0]
+    if k_rope.shape[0] != T:
+        raise TypeError("latent and k_rope must have the same number of rows")
+    _shaped(_i32(positions, "positions"), "positions", torch.int32, (T,))
+    _shaped(_i32(slots, "slots"), "slots", torch.int32, (T,))
+    _shaped(_freqs(freqs), "freqs", torch.float64, (32,))
+    H = qt = qh = ot = oh = 0
+    if q_rope is not None:
+        if q_out is None:
+            q_out = torch.empty(q_rope.shape, dtype=q_rope.dtype, device=q_rope.device)
+        for name, t in (("q_rope", q_rope), ("q_out", q_out)):
+            if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != T or t.shape[2] != 64:
+                raise TypeError(f"{name} must be a bf16 [T, H, 64] tensor")
+        if q_out.shape != q_rope.shape:
+            raise TypeError("q_rope and q_out must have the same shape")
+        _, H, _, qt, qh = _rows3(q_rope, "q_rope")
+        _, _, _, ot, oh = _rows3(q_out, "q_out")
+    elif q_out is not None:
+        raise TypeError("q_out needs q_rope")
+    _on_device(latent.device, k_rope=k_rope, positions=positions, slots=slots, kv=kv.data, freqs=freqs, q_rope=q_rope,
+               q_out=q_out)
+    _cache_fits(kv)
+    ws = default_workspace() if ws is None else ws
+    kvc = kv._c()
+    lat_stride = latent.stride(0) if T > 1 else 512
+    kr_stride = k_rope.stride(0) if T > 1 else 64
+    with_q = q_rope is not None and H > 0
+    _check(lib().svt_rope_append(_ptr(latent), lat_stride, _ptr(k_rope), kr_stride, _ptr(positions), _ptr(slots), T,
+                                 ctypes.byref(kvc), _ptr(freqs), _choice(layout, ROPE_LAYOUTS, "layout"),
+                                 float(amplitude), _ptr(q_rope) if with_q else None, H, qt, qh,
+                                 _ptr(q_out) if with_q else None, ot, oh, ws.ptr, ws.nbytes, _stream()),
+           "svt_rope_append")
+    return q_out
+
+
+def _cache_fits(kv: KVCache) -> None:
+    """The cache's tensor holds the rows its descriptor promises."""
+    row = kv.row_stride_bytes or ROW_BYTES.get(kv.dtype, 0)
+    if kv.num_slots and kv.data.numel() * kv.data.element_size() < (kv.num_slots - 1) * row + ROW_BYTES.get(kv.dtype, 0):
+        raise TypeError("kv data is smaller than num_pages * page_size rows")
+
+
+def sparse_mla_backward(q, kv: KVCache, topk, softmax_scale: float, out, lse, dout, *, dlse=None, block_table=None,
+                        seq_lens=None, req_of_token=None, topk_len=None, dq=None, dkv=None,
+                        return_weights: bool = False, ws: Optional[Workspace] = None):
+    """svt_sparse_mla_backward: the gradients of sparse_mla_decode (or of a grouped prefill, with each
+    query's own list). out and lse are the forward's; dout (and dlse) their gradients. Returns
+    (dq [T, H, 576] bf16, dkv [num_slots, 576] bf16, weights [T, K] fp32 or None)."""
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != 576 or not q.is_contiguous():
+        raise TypeError("q must be a contiguous bf16 [T, H, 576] tensor")
+    T, H, _ = q.shape
+    topk = _i32(topk, "topk")
+    if topk.dim() != 2 or topk.shape[0] != T:
+        raise TypeError("topk must be an int32 [T, K] tensor")
+    K = topk.shape[1]
+    _shaped(out, "out", torch.bfloat16, (T, H, 512))
+    _shaped(dout, "dout", torch.bfloat16, (T, H, 512))
+    _shaped(lse, "lse", torch.float32, (T, H))
+    _shaped(dlse, "dlse", torch.float32, (T, H))
+    bt = _i32(block_table, "block_table")
+    if bt is not None and bt.dim() != 2:
+        raise TypeError("block_table must be [num_reqs, max_blocks]")
+    if bt is not None and seq_lens is not None:
+        _shaped(_i32(seq_lens, "seq_lens"), "seq_lens", torch.int32, (bt.shape[0],))
+    _shaped(_i32(req_of_token, "req_of_token"), "req_of_token", torch.int32, (T,))
+    _shaped(_i32(topk_len, "topk_len"), "topk_len", torch.int32, (T,))
+    if dq is None:
+        dq = torch.empty((T, H, 576), dtype=torch.bfloat16, device=q.device)
+    if dkv is None:
+        dkv = torch.empty((kv.num_slots, 576), dtype=torch.bfloat16, device=q.device)
+    _shaped(dq, "dq", torch.bfloat16, (T, H, 576))
+    _shaped(dkv, "dkv", torch.bfloat16, (kv.num_slots, 576))
+    weights = torch.empty((T, K), dtype=torch.float32, device=q.device) if return_weights else None
+    _on_device(q.device, kv=kv.data, topk=topk, out=out, lse=lse, dout=dout, dlse=dlse, block_table=bt,
+               seq_lens=seq_lens, req_of_token=req_of_token, topk_len=topk_len, dq=dq, dkv=dkv)
+    _cache_fits(kv)
+    ws = (ws or default_workspace()).ensure(lib().svt_sparse_mla_backward_workspace_size(T, H, K, kv.num_slots))
+    kvc = kv._c()
+    _check(lib().svt_sparse_mla_backward(_ptr(q), T, H, ctypes.byref(kvc), _ptr(bt), 0 if bt is None else bt.shape[0],
+                                         0 if bt is None else bt.shape[1], _ptr(req_of_token), _ptr(seq_lens),
+                                         _ptr(topk), K, _ptr(topk_len), float(softmax_scale), _ptr(out), _ptr(lse),
+                                         _ptr(dout), _ptr(dlse), _ptr(dq), _ptr(dkv), _ptr(weights), ws.ptr, ws.nbytes,
+                                         _stream()), "svt_sparse_mla_backward")
+    return dq, dkv, weights
+
+
+def distill_topk(scores, topk, teacher, *, lens=None, temperature: float = 1.0, teacher_kind: str = "weights",
+                 over: str = "candidates", row_weight=None, need_grad: bool = True, dscores=None):
+    """svt_distill_topk: per query, KL(teacher's top entries || softmax of scores) and the gradient of
+    row_weight . loss. scores [T, N] fp32 or bf16 (rows may be strided), topk [T, K] positions (-1 =
+    none), teacher [T, K] fp32 weights or logits. Returns (loss [T], dscores [T, N] or None)."""
+    if scores.dtype not in (torch.float32, torch.bfloat16) or scores.dim() != 2 or (
+            scores.shape[1] > 1 and scores.stride(1) != 1):
+        raise TypeError("scores must be an fp32 or bf16 [T, N] tensor with unit column stride")
+    T, N = scores.shape
+    topk = _i32(topk, "topk")
+    if topk.dim() != 2 or topk.shape[0] != T:
+        raise TypeError("topk must be an int32 [T, K] tensor")
+    K = topk.shape[1]
+    _shaped(teacher, "teacher", torch.float32, (T, K))
+    _shaped(_i32(lens, "lens"), "lens", torch.int32, (T,))
+    _shaped(row_weight, "row_weight", torch.float32, (T,))
+    loss = torch.empty((T,), dtype=torch.float32, device=scores.device)
+    if dscores is None and need_grad:
+        dscores = torch.empty((T, N), dtype=scores.dtype, device=scores.device)
+    if dscores is not None and (dscores.dtype != scores.dtype or dscores.shape != scores.shape or (
+            N > 1 and dscores.stride(1) != 1)):
+        raise TypeError("dscores must have scores' type and shape, with unit column stride")
+    _on_device(scores.device, topk=topk, teacher=teacher, lens=lens, row_weight=row_weight, dscores=dscores)
+    stride = scores.stride(0) if T > 1 else N  # a single row's stride is meaningless (can be 0)
+    dstride = dscores.stride(0) if dscores is not None and T > 1 else N
+    _check(lib().svt_distill_topk(_ptr(scores), 1 if scores.dtype == torch.float32 else 0, T, N, stride, _ptr(lens),
+                                  _ptr(topk), _ptr(teacher), K, _choice(teacher_kind, TEACHER_KINDS, "teacher_kind"),
+                                  _choice(over, DISTILL_SCOPES, "over"), float(temperature), _ptr(row_weight),
+                                  _ptr(loss), _ptr(dscores), dstride, _stream()), "svt_distill_topk")
+    return loss, dscores
 
 
 def debug_pipeline_fault(fault: int = 0, wait_limit_ns: int = 0) -> None:

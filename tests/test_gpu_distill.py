@@ -1,0 +1,173 @@
+"""The distillation loss on a teacher's top entries and its gradient, against fp64."""
+
+import math
+
+import pytest
+import torch
+
+from tests import _layer_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def S():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import sparse_mla_attention_top_gb300 as S
+    from sparse_mla_attention_top_gb300 import build
+
+    build.build()
+    return S
+
+
+def case(seed, T, N, K, dtype=torch.float32, kind="weights", ragged=True):
+    g = torch.Generator().manual_seed(seed)
+    scores = (torch.randn((T, N), generator=g) * 3).to(dtype)
+    lens = torch.randint(0, N + 1, (T,), generator=g, dtype=torch.int32) if ragged else None
+    if ragged:
+        lens[-1] = N
+        lens[0] = min(N, 1)
+    topk = torch.full((T, K), -1, dtype=torch.int32)
+    for t in range(T):
+        n = N if lens is None else int(lens[t])
+        m = min(K, n)
+        topk[t, :m] = torch.randperm(n, generator=g)[:m].to(torch.int32)
+    value = torch.randn((T, K), generator=g) * 2
+    return scores, lens, topk, torch.exp(value) if kind == "weights" else value
+
+
+def check(S, scores, lens, topk, teacher, kind="weights", scope="candidates", temperature=1.0, row_weight=None,
+          scores_dev=None, dscores=None):
+    dev = lambda t: None if t is None else t.cuda()  # noqa: E731
+    loss, grad = S.distill_topk(dev(scores) if scores_dev is None else scores_dev, dev(topk), dev(teacher), lens=dev(lens),
+                                temperature=temperature, teacher_kind=kind, over=scope, row_weight=dev(row_weight),
+                                dscores=dscores)
+    (rl, rg), (bl, bg) = R.distill(scores, lens, topk, teacher, kind, scope, temperature, row_weight)
+    R.within(loss, rl, bl, "loss")
+    half = R.HALF[scores.dtype]
+    # a value below the type's normal range is held to its smallest step (fp32 and bf16: 2^-126)
+    R.within(grad, rg, bg + half * (rg.abs() + bg) + 2.0 ** -126, "gradient")
+    return loss, grad
+
+
+@pytest.mark.parametrize("scope", ["candidates", "listed"])
+@pytest.mark.parametrize("kind", ["weights", "logits"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,N,K", [(1, 1, 1), (3, 5, 8), (7, 333, 40), (5, 4096, 512), (2, 20000, 2048)])
+def test_distill(S, scope, kind, dtype, T, N, K):
+    s, lens, topk, w = case(T * N, T, N, K, dtype, kind)
+    rw = torch.linspace(-0.5, 2.0, T)
+    check(S, s, lens, topk, w, kind, scope, 0.7, rw)
+
+
+@pytest.mark.parametrize("scope", ["candidates", "listed"])
+@pytest.mark.parametrize("T,N", [(400, 16384), (400, 16390), (1, 131072), (2, 140001), (330, 33000)])
+def test_distill_whole_rows_and_rows_beyond_shared_memory(S, scope, T, N):
+    """One CTA a row up to 16384 scores, up to eight of them, and rows longer than eight parts."""
+    g = torch.Generator().manual_seed(5)
+    s = torch.randn((T, N), generator=g)
+    topk = torch.randint(0, N, (T, 33), generator=g, dtype=torch.int32).sort(1).values
+    w = torch.rand((T, 33), generator=g)
+    lens = torch.full((T,), N, dtype=torch.int32)
+    lens[T // 2] = N // 2
+    loss, grad = S.distill_topk(s.cuda(), topk.cuda(), w.cuda(), lens=lens.cuda(), over=scope)
+    pick = sorted({0, T // 2, T - 1})
+    (rl, rg), (bl, bg) = R.distill(s[pick], lens[pick], topk[pick], w[pick], "weights", scope, 1.0)
+    R.within(loss[pick], rl, bl, "loss")
+    R.within(grad[pick], rg, bg + 2.0 ** -24 * rg.abs() + 2.0 ** -126, "gradient")
+
+
+def test_distill_no_lens_no_row_weight_and_loss_or_gradient_alone(S):
+    s, _, topk, w = case(1, 6, 777, 30, ragged=False)
+    loss, grad = check(S, s, None, topk, w)
+    only, none = S.distill_topk(s.cuda(), topk.cuda(), w.cuda(), need_grad=False)
+    assert none is None and torch.equal(only, loss)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_distill_strided_rows_leave_what_lies_between(S, dtype):
+    s, lens, topk, w = case(2, 6, 130, 20, dtype)
+    for lead, stride in ((0, 136), (1, 139), (4, 160)):
+        wide = torch.zeros(6, stride, dtype=dtype, device="cuda")
+        wide[:, lead:lead + 130] = s.cuda()
+        out = torch.full((6, stride), 9.0, dtype=dtype, device="cuda")
+        check(S, s, lens, topk, w, scores_dev=wide[:, lead:lead + 130], dscores=out[:, lead:lead + 130])
+        out[:, lead:lead + 130] = 9
+        assert bool((out == 9).all())
+
+
+@pytest.mark.parametrize("scope", ["candidates", "listed"])
+def test_distill_rows_with_nothing(S, scope):
+    T, N, K = 6, 50, 4
+    s = torch.randn(T, N, generator=torch.Generator().manual_seed(3))
+    topk = torch.tensor([[0, 1, 2, 3]] * T, dtype=torch.int32)
+    w = torch.ones(T, K)
+    lens = torch.tensor([0, 50, 50, 50, 50, -3], dtype=torch.int32)
+    topk[1] = -1                     # no entry
+    w[2] = 0                         # no weight
+    topk[3] = torch.tensor([50, 60, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32)  # all outside
+    s[4] = -math.inf                 # no score
+    loss, grad = check(S, s, lens, topk, w, scope=scope)
+    assert not loss.any() and not grad.any()
+    logits = torch.full((T, K), -math.inf)
+    loss, grad = check(S, s, lens, topk, logits, kind="logits", scope=scope)
+    assert not loss.any() and not grad.any()
+
+
+@pytest.mark.parametrize("scope", ["candidates", "listed"])
+def test_distill_masked_scores_and_weights(S, scope):
+    T, N, K = 3, 100, 6
+    s = torch.randn(T, N, generator=torch.Generator().manual_seed(4))
+    topk = torch.arange(6, dtype=torch.int32).repeat(T, 1)
+    w = torch.rand(T, K, generator=torch.Generator().manual_seed(5)) + 0.1
+    s[0, 10:] = -math.inf
+    s[0, 2] = -math.inf
+    w[0, 2] = 0.0                    # a masked score whose weight is 0 costs nothing
+    s[1, 3:5] = torch.finfo(torch.float32).min
+    w[1, 3:5] = 0.0
+    s[2, 50] = 80.0
+    check(S, s, None, topk, w, scope=scope, temperature=2.0)
+    w[0, 2] = 1.0                    # with a weight, it costs everything, in its own row alone
+    loss, grad = S.distill_topk(s.cuda(), topk.cuda(), w.cuda(), over=scope)
+    assert math.isinf(loss[0]) and bool(torch.isfinite(loss[1:]).all()) and bool(torch.isfinite(grad).all())
+    s[1, 1] = math.nan
+    loss, grad = S.distill_topk(s.cuda(), topk.cuda(), w.cuda(), over=scope)
+    assert math.isnan(loss[1]) and math.isfinite(loss[2]) and bool(torch.isfinite(grad[2]).all())
+
+
+@pytest.mark.parametrize("scope", ["candidates", "listed"])
+def test_distill_positions_listed_twice_count_twice(S, scope):
+    s, _, _, _ = case(6, 2, 40, 6, ragged=False)
+    topk = torch.tensor([[5, 5, 7, -1, 5, 9], [39, 0, 0, 39, 1, 1]], dtype=torch.int32)
+    check(S, s, None, topk, torch.rand(2, 6, generator=torch.Generator().manual_seed(7)), scope=scope)
+
+
+@pytest.mark.parametrize("scope", ["candidates", "listed"])
+def test_distill_gradient_matches_differences(S, scope):
+    """The fp64 loss along a direction, by a central difference of step h = 1e-4: its own error is h^2 / 6
+    times a third derivative below 10 |d|^3, and 2^-50 / h."""
+    s, lens, topk, w = case(8, 5, 200, 20)
+    rw = torch.rand(5, generator=torch.Generator().manual_seed(9))
+    d = torch.randn(5, 200, generator=torch.Generator().manual_seed(10)).double()
+    _, grad = S.distill_topk(s.cuda(), topk.cuda(), w.cuda(), lens=lens.cuda(), row_weight=rw.cuda(), over=scope)
+    h = 1e-4
+    up, down = (R.distill(s.double() + z * h * d, lens, topk, w, "weights", scope, 1.0)[0][0] for z in (1, -1))
+    num = ((up - down) / (2 * h) * rw.double()).sum()
+    ana = (grad.double().cpu() * d).sum()
+    assert abs(float(num - ana)) <= 2.0 ** -18 * float((grad.double().cpu() * d).abs().sum()) + 1e-6
+
+
+def test_distill_in_a_graph(S):
+    s, lens, topk, w = case(11, 8, 3000, 64)
+    a, b, c, n = s.cuda(), topk.cuda(), w.cuda(), lens.cuda()
+    S.distill_topk(a, b, c, lens=n)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        loss, grad = S.distill_topk(a, b, c, lens=n)
+    s2, lens2, topk2, w2 = case(12, 8, 3000, 64)
+    for x, y in ((a, s2), (b, topk2), (c, w2), (n, lens2)):
+        x.copy_(y)
+    g.replay()
+    want = S.distill_topk(a, b, c, lens=n)
+    assert torch.equal(loss, want[0]) and torch.equal(grad, want[1])
