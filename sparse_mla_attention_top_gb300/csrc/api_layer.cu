@@ -58,15 +58,25 @@ bool rows_overlap(int32_t T, int32_t H, int32_t D, int64_t st, int64_t sh) {
   return false;
 }
 
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  return sms;
+}
+
+// Workspace: status header | slots | list reaches | (lse, delta) | cut row-sets' dq | cache rows' sums.
 struct BackwardWs {
-  size_t slots, dq, dkv, end;
+  size_t slots, live_len, stats, part, acc, end;
 };
-BackwardWs backward_ws(int32_t T, int32_t H, int32_t K, int64_t num_slots) {
+BackwardWs backward_ws(const svt::BackwardParams& p) {
   BackwardWs w;
   w.slots = svt::kStatusBytes;
-  w.dq = w.slots + round_up(static_cast<size_t>(T) * K * 4, 256);
-  w.dkv = w.dq + round_up(static_cast<size_t>(T) * H * svt::kRow * 4, 256);
-  w.end = w.dkv + round_up(static_cast<size_t>(num_slots) * svt::kRow * 4, 256);
+  w.live_len = w.slots + round_up(static_cast<size_t>(p.T) * p.K * 4, 256);
+  w.stats = w.live_len + round_up(static_cast<size_t>(p.T) * 4, 256);
+  w.part = w.stats + round_up(static_cast<size_t>(p.T) * p.H * 8, 256);
+  w.acc = w.part + 2ull * p.num_ctas * 64 * svt::kRow * 4;
+  w.end = w.acc + round_up(static_cast<size_t>(p.num_slots) * svt::kRow * 4, 256);
   return w;
 }
 
@@ -222,7 +232,13 @@ svt_status svt_rope_append(const void* latent_bf16, int64_t latent_stride, const
 
 size_t svt_sparse_mla_backward_workspace_size(int32_t T, int32_t H, int32_t K, int64_t num_slots) {
   if (T < 0 || H < 0 || K < 0 || num_slots < 0) return svt::kStatusBytes;
-  return backward_ws(T, H, K, num_slots).end;
+  svt::BackwardParams p{};
+  p.T = T;
+  p.H = H;
+  p.K = K;
+  p.num_slots = num_slots;
+  svt::plan_backward(p, sm_count());
+  return backward_ws(p).end;
 }
 
 svt_status svt_sparse_mla_backward(const void* q_bf16, int32_t T, int32_t H, const svt_kv_cache* kv,
@@ -242,9 +258,15 @@ svt_status svt_sparse_mla_backward(const void* q_bf16, int32_t T, int32_t H, con
   if (block_table != nullptr && (num_reqs <= 0 || max_blocks <= 0))
     return set_last_error(SVT_ERR_INVALID_ARG, "num_reqs and max_blocks must be > 0 with a block table");
   const long long num_slots = kv->num_pages * static_cast<long long>(kv->page_size);
-  if (static_cast<long long>(T) * H >= (1ll << 31) || static_cast<long long>(T) * ((K + 15) / 16) >= (1ll << 31))
-    return set_last_error(SVT_ERR_UNSUPPORTED, "T * H and T * K / 16 must be below 2^31");
-  const BackwardWs w = backward_ws(T, H, K, num_slots);
+  if (static_cast<long long>(T) * H >= (1ll << 31) || static_cast<long long>(T) * K >= (1ll << 40))
+    return set_last_error(SVT_ERR_UNSUPPORTED, "T * H must be below 2^31 and T * K below 2^40");
+  svt::BackwardParams p{};
+  p.T = T;
+  p.H = H;
+  p.K = K;
+  p.num_slots = num_slots;
+  svt::plan_backward(p, sm_count());
+  const BackwardWs w = backward_ws(p);
   st = svt::check_workspace(ws, ws_bytes, w.end);
   if (st != SVT_OK) return st;
   if (dkv_bf16 == nullptr || !aligned(dkv_bf16, 16))
@@ -256,15 +278,6 @@ svt_status svt_sparse_mla_backward(const void* q_bf16, int32_t T, int32_t H, con
       return set_last_error(SVT_ERR_INVALID_ARG, "q, out, dout and dq must be 16-byte aligned");
     if (K > 0 && topk == nullptr) return set_last_error(SVT_ERR_INVALID_ARG, "topk must not be null");
   }
-  char* base = static_cast<char*>(ws);
-  int32_t* slots = reinterpret_cast<int32_t*>(base + w.slots);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaMemsetAsync(base + w.dq, 0, w.end - w.dq, s);
-  if (e == cudaSuccess && T > 0 && K > 0)
-    e = svt::launch_resolve(topk, T, K, topk_len, req_of_token, block_table, num_reqs, max_blocks, seq_lens,
-                            kv->page_size, kv->num_pages, slots, static_cast<int*>(ws), s);
-  if (e != cudaSuccess) return cuda_fail(e, "svt_sparse_mla_backward (lists)");
-  svt::BackwardParams p{};
   p.q = static_cast<const uint16_t*>(q_bf16);
   p.out = static_cast<const uint16_t*>(out_bf16);
   p.dout = static_cast<const uint16_t*>(dout_bf16);
@@ -272,19 +285,21 @@ svt_status svt_sparse_mla_backward(const void* q_bf16, int32_t T, int32_t H, con
   p.dlse = dlse;
   p.kv = static_cast<const uint8_t*>(kv->data);
   p.row_stride = row_stride;
-  p.num_slots = num_slots;
-  p.T = T;
-  p.H = H;
-  p.K = K;
   p.scale = softmax_scale;
-  p.slots = slots;
   p.dq = static_cast<uint16_t*>(dq_bf16);
   p.dkv = static_cast<uint16_t*>(dkv_bf16);
   p.weights = weights;
-  p.dq_acc = reinterpret_cast<float*>(base + w.dq);
-  p.dkv_acc = reinterpret_cast<float*>(base + w.dkv);
+  char* base = static_cast<char*>(ws);
+  p.slots = reinterpret_cast<int32_t*>(base + w.slots);
+  p.live_len = reinterpret_cast<int32_t*>(base + w.live_len);
+  p.stats = reinterpret_cast<float2*>(base + w.stats);
+  p.dq_part = reinterpret_cast<float*>(base + w.part);
+  p.dkv_acc = reinterpret_cast<float*>(base + w.acc);
   p.status = static_cast<int*>(ws);
-  e = svt::launch_backward(p, s);
+  svt::debug_fault_state(&p.fault, &p.wait_limit_ns);
+  const svt::ListParams lists{topk,     topk_len,      req_of_token, block_table, num_reqs, max_blocks,
+                              seq_lens, kv->page_size, kv->num_pages};
+  const cudaError_t e = svt::launch_backward(p, lists, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "svt_sparse_mla_backward");
   return SVT_OK;
 }

@@ -5,135 +5,552 @@
 // and a cache row's gradient is the sum of dK (+ dV on the latent columns) over the lists that
 // hold it. sum over heads of P is each entry's attention weight.
 //
-// One CTA per (query, 16 list entries): the rows stay in shared memory as fp32, heads go one
-// after another, each thread owns three channels of the 16 rows' gradients.
+// Three kernels. prepare resolves the lists and forms delta and lse in log2 units. The main
+// kernel walks (row-set, 64-entry tile) pairs, a row-set being up to 64 heads of one query, one
+// persistent CTA per SM with an equal share of all tiles (stream-K). finish joins the dq of
+// row-sets cut between CTAs (fp32, in a fixed order) and rounds the cache rows' sums to bf16.
+//
+// Main kernel, per tile, on tcgen05 with fp32 accumulators in tensor memory (e = entry, r = head
+// row, c = channel; the contractions' operands are the tiles as they lie, read K- or MN-major):
+//   1. [S^T | dP^T][e, r]  = K [q | dout]^T     one 64 x 128 product: q and dout lie interleaved
+//                                               in 64-channel blocks, so both share the reads of K
+//   2. dq^T[c, r]         += K^T dS             stays in tensor memory over the row-set's tiles
+//   3. dKV^T[c, e]         = q^T dS + dout^T P  128 channels at a time; each block leaves for
+//                                               fp32 atomic additions as it is done
+// Lane = channel in 3, so a warp adds 128 contiguous bytes of one cache row per instruction.
+//
+// Warps: 8 softmax (S^T, dP^T -> P, dS in bf16; dq out), 8 scatter (dKV^T -> additions), 3 gather
+// (cp.async, rows zero-filled where there is none), 1 that issues the MMAs. q and dout (136 KB)
+// and one 72 KB tile of rows fill shared memory, so the next tile is gathered while step 3 runs.
 #include <math_constants.h>
 
 #include <cstdint>
 
 #include "device.cuh"
 #include "internal.h"
+#include "resolve_entry.cuh"
 
 namespace svt {
 
 namespace {
 
-constexpr int kTile = 16;
-constexpr int kThreads = 192;  // 3 channels each
-constexpr int kWarps = kThreads / 32;
+constexpr int kRows = 64;     // heads of a row-set
+constexpr int kEntries = 64;  // list entries of a tile
+constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+// shared memory (bytes from a 1024-byte boundary): 64 x 64 bf16 blocks in the 128-byte swizzle
+constexpr uint32_t kBlk = 8192;
+constexpr uint32_t kOffQ = 0;            // q0 dout0 q1 dout1 .. q7 dout7 q8
+constexpr uint32_t kOffKv = 17 * kBlk;   // 9 blocks
+constexpr uint32_t kOffP = kOffKv + 9 * kBlk;
+constexpr uint32_t kOffDs = kOffP + kBlk;
+constexpr uint32_t kOffMisc = kOffDs + kBlk;
+struct Misc {
+  int slot[4][kEntries];  // the tile's cache rows, a ring: scatter may trail the gather by two tiles
+  float weight[kEntries];
+  uint64_t bars[16];
+  uint32_t tmem;
+  int abort_flag;
+};
+constexpr uint32_t kSmem = kOffMisc + sizeof(Misc) + 1024;
+static_assert(kSmem <= 232448, "backward shared memory");
 
-__global__ void __launch_bounds__(kThreads) backward_kernel(const BackwardParams p) {
-  __shared__ float rows[kTile][kRow];
-  __shared__ float qs[kRow], dos[kVdim];
-  __shared__ float pr[kTile], ds[kTile];
-  __shared__ int slot[kTile];
-  __shared__ float delta_s;
-  __shared__ float dred[kWarps];
-  const int tiles = (p.K + kTile - 1) / kTile;
-  const int t = blockIdx.x / tiles, j0 = (blockIdx.x - t * tiles) * kTile;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid < kTile) slot[tid] = j0 + tid < p.K ? p.slots[static_cast<long long>(t) * p.K + j0 + tid] : -1;
-  __syncthreads();
-  for (int i = tid; i < kTile * kRow; i += kThreads) {
-    const int e = i / kRow, c = i - e * kRow;
-    rows[e][c] = slot[e] >= 0
-                     ? bf(reinterpret_cast<const uint16_t*>(p.kv + slot[e] * p.row_stride)[c])
-                     : 0.f;
+// barriers
+enum { kBarKvFull, kBarKvFree, kBarS, kBarP, kBarSeg, kBarDq, kBarDqFree, kBarChunk, kBarChunkFree = kBarChunk + 3,
+       kBarDone = kBarChunkFree + 3, kNumBars };
+static_assert(kNumBars <= 16, "barriers");
+
+// tensor memory columns: dq^T in five blocks of 64 (channels 128 mb .. +127, then the 64 rope
+// ones), S^T and dP^T, and a block for dKV^T; the S^T and dP^T columns serve as two more once
+// the softmax has read them
+constexpr uint32_t kTmDq = 0, kTmS = 320, kTmX = 448;
+
+constexpr int kSoftWarps = 8, kScatWarps = 8, kFillWarps = 3;
+constexpr int kScatWarp0 = kSoftWarps, kFillWarp0 = kScatWarp0 + kScatWarps, kMmaWarp = kFillWarp0 + kFillWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kFillThreads = 32 * kFillWarps;
+constexpr int kFillStep = kFillThreads / 8;                       // rows filled at once, 8 threads each
+constexpr int kFillRows = (kRows + kFillStep - 1) / kFillStep;  // rows per thread
+
+constexpr uint32_t kIdescS = idesc_f32acc(64, 128, 0, 0, kFmtBf16);
+constexpr uint32_t kIdescSRope = idesc_f32acc(64, 64, 0, 0, kFmtBf16);
+constexpr uint32_t kIdescDq = idesc_f32acc(128, 64, 1, 1, kFmtBf16);
+constexpr uint32_t kIdescDqRope = idesc_f32acc(64, 64, 1, 1, kFmtBf16);
+constexpr uint32_t kIdescKv = idesc_f32acc(128, 64, 1, 0, kFmtBf16);
+constexpr uint32_t kIdescKvRope = idesc_f32acc(64, 64, 1, 0, kFmtBf16);
+
+// The part of one row-set that this CTA walks: live tiles j0 .. j1 - 1 (none when j0 >= j1).
+struct Seg {
+  int rowset, t;
+  long long base;  // first of its rows in [T * H, ...]
+  int nvalid;
+  int j0, j1;
+  bool whole;      // this CTA has every tile of the row-set
+  int part;        // where its dq goes otherwise
+};
+
+// Walks the segments of CTA blockIdx.x; every role runs its own copy.
+struct SegIter {
+  const BackwardParams& p;
+  long long pos, hi;
+  __device__ explicit SegIter(const BackwardParams& q) : p(q) {
+    pos = streamk_lo(blockIdx.x, p.total_tiles, p.num_ctas);
+    hi = streamk_lo(blockIdx.x + 1ll, p.total_tiles, p.num_ctas);
   }
-  float acc[kTile][3] = {};
-  float wsum = 0.f;  // thread e < 16: entry e's weight
-  for (int h = 0; h < p.H; ++h) {
-    const long long r = static_cast<long long>(t) * p.H + h;
-    __syncthreads();
-    float d = 0.f;
-    for (int c = tid; c < kRow; c += kThreads) qs[c] = bf(p.q[r * kRow + c]);
-    for (int c = tid; c < kVdim; c += kThreads) {
-      const float g = bf(p.dout[r * kVdim + c]);
-      dos[c] = g;
-      d += g * bf(p.out[r * kVdim + c]);
-    }
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if (lane == 0) dred[warp] = d;
-    __syncthreads();
-    if (tid == 0) {
-      float s = p.dlse ? -p.dlse[r] : 0.f;
-      for (int w = 0; w < kWarps; ++w) s += dred[w];
-      delta_s = s;
-    }
-    __syncthreads();
-    const float lse = p.lse[r];
-    for (int e = warp; e < kTile; e += kWarps) {
-      float s = 0.f, dp = 0.f;
-      for (int c = lane; c < kRow; c += 32) {
-        s += qs[c] * rows[e][c];
-        if (c < kVdim) dp += dos[c] * rows[e][c];
-      }
-      for (int o = 16; o > 0; o >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, o);
-        dp += __shfl_xor_sync(0xffffffffu, dp, o);
-      }
-      if (lane == 0) {
-        const float pe = slot[e] >= 0 && lse != -CUDART_INF_F ? expf(s * p.scale - lse) : 0.f;
-        pr[e] = pe;
-        ds[e] = pe != 0.f ? pe * (dp - delta_s) * p.scale : 0.f;
-      }
-    }
-    __syncthreads();
-    if (tid < kTile) wsum += pr[tid];
-#pragma unroll
-    for (int u = 0; u < 3; ++u) {
-      const int c = tid + u * kThreads;
-      float dq = 0.f;
-      const float qc = qs[c], doc = c < kVdim ? dos[c] : 0.f;
-#pragma unroll
-      for (int e = 0; e < kTile; ++e) {
-        dq += ds[e] * rows[e][c];
-        acc[e][u] += ds[e] * qc + pr[e] * doc;
-      }
-      if (dq != 0.f) atomicAdd(p.dq_acc + r * kRow + c, dq);
-    }
+  __device__ bool next(Seg& s) {
+    if (pos >= hi) return false;
+    const int r = static_cast<int>(pos / p.tiles);
+    const long long first = static_cast<long long>(r) * p.tiles;
+    const long long end = first + p.tiles < hi ? first + p.tiles : hi;
+    s.rowset = r;
+    s.t = r / p.hchunks;
+    const int chunk = r - s.t * p.hchunks;
+    s.base = static_cast<long long>(s.t) * p.H + chunk * kRows;
+    s.nvalid = min(kRows, p.H - chunk * kRows);
+    const int live = (p.live_len[s.t] + kEntries - 1) / kEntries;
+    s.j0 = static_cast<int>(pos - first);
+    s.j1 = min(static_cast<int>(end - first), live);
+    s.whole = pos == first && end == first + p.tiles;
+    s.part = static_cast<int>(streamk_part_slot(blockIdx.x, first, p.total_tiles, p.num_ctas));
+    pos = end;
+    return true;
   }
+};
+
+__device__ __forceinline__ void gather_role(const BackwardParams& p, uint8_t* smem, Misc* misc, uint32_t bars,
+                                            const WaitCtl& wc) {
+  const int tid = static_cast<int>(threadIdx.x) - 32 * kFillWarp0;
+  const uint32_t base = smem_u32(smem);
+  const int c = tid & 7, r0 = tid >> 3;  // 16-byte chunk of a block, first row
+  auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
+  uint32_t g = 0, segs = 0;
+  SegIter it(p);
+  Seg s;
+  while (it.next(s)) {
+    if (s.j0 >= s.j1) continue;
+    // the last segment's products are done: q and dout may be replaced
+    if (segs > 0) mbar_wait(bar(kBarSeg), (segs - 1) & 1, wc);
+    for (int r = r0; r < kRows; r += kFillStep) {
+      const uint32_t ok = r < s.nvalid ? 16u : 0u;
+      const uint16_t* q = p.q + (s.base + (ok ? r : 0)) * kRow + c * 8;
+      const uint16_t* d = p.dout + (s.base + (ok ? r : 0)) * kVdim + c * 8;
+      const uint32_t at = base + kOffQ + sw128_offset(r, c);
 #pragma unroll
-  for (int e = 0; e < kTile; ++e)
-    if (slot[e] >= 0)
+      for (int kb = 0; kb < 8; ++kb) {
+        cp_async16(at + 2 * kb * kBlk, q + 64 * kb, ok);
+        cp_async16(at + (2 * kb + 1) * kBlk, d + 64 * kb, ok);
+      }
+      cp_async16(at + 16 * kBlk, q + 512, ok);
+    }
+    const int32_t* list = p.slots + static_cast<long long>(s.t) * p.K;
+    int slot[kFillRows];
+    auto load_slots = [&](int j) {
 #pragma unroll
-      for (int u = 0; u < 3; ++u)
-        atomicAdd(p.dkv_acc + static_cast<long long>(slot[e]) * kRow + tid + u * kThreads, acc[e][u]);
-  if (p.weights != nullptr && tid < kTile && j0 + tid < p.K)
-    p.weights[static_cast<long long>(t) * p.K + j0 + tid] = wsum;
+      for (int i = 0; i < kFillRows; ++i) {
+        const int r = r0 + kFillStep * i, k = j * kEntries + r;
+        slot[i] = r < kEntries && k < p.K ? __ldg(list + k) : -1;
+      }
+    };
+    load_slots(s.j0);
+    for (int j = s.j0; j < s.j1; ++j, ++g) {
+      if (j > s.j0) mbar_wait(bar(kBarKvFree), (g - 1) & 1, wc);
+#pragma unroll
+      for (int i = 0; i < kFillRows; ++i) {
+        const int r = r0 + kFillStep * i;
+        if (r >= kEntries) break;
+        const uint32_t ok = slot[i] >= 0 ? 16u : 0u;
+        const uint8_t* row = p.kv + (ok ? slot[i] * p.row_stride : 0) + c * 16;
+        const uint32_t at = base + kOffKv + sw128_offset(r, c);
+#pragma unroll
+        for (int kb = 0; kb < 9; ++kb) cp_async16(at + kb * kBlk, row + 128 * kb, ok);
+        if (c == 0) misc->slot[g & 3][r] = slot[i];
+      }
+      if (j + 1 < s.j1) load_slots(j + 1);
+      cp_async_wait_all();
+      fence_proxy_async_smem();  // the rows (generic proxy) -> MMA operand reads
+      if (!(g == 0 && (p.fault & kFaultWithholdFirstFill))) mbar_arrive(bar(kBarKvFull));
+    }
+    ++segs;
+  }
 }
 
-// fp32 sums -> bf16, eight at a time.
-__global__ void __launch_bounds__(256) round_kernel(const float* __restrict__ src, uint16_t* __restrict__ dst,
-                                                    long long n8) {
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n8; i += gridDim.x * 256ll) {
-    const float4 a = reinterpret_cast<const float4*>(src)[2 * i], b = reinterpret_cast<const float4*>(src)[2 * i + 1];
-    reinterpret_cast<uint4*>(dst)[i] = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
-                                                  pack_bf16x2(b.z, b.w));
+__device__ __forceinline__ void mma_role(const BackwardParams& p, uint8_t* smem, uint32_t tmem, uint32_t bars,
+                                         const WaitCtl& wc) {
+  const uint32_t base = smem_u32(smem);
+  const uint32_t qb = base + kOffQ, kv = base + kOffKv, pb = base + kOffP, ds = base + kOffDs;
+  auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
+  uint32_t g = 0, segs = 0;
+  bool ok = true;
+  SegIter it(p);
+  Seg s;
+  while (ok && it.next(s)) {
+    if (s.j0 >= s.j1) continue;
+    for (int j = s.j0; ok && j < s.j1; ++j, ++g) {
+      ok = mbar_wait(bar(kBarKvFull), g & 1, wc);
+      // the S^T and dP^T columns last held the previous tile's fourth and fifth blocks
+      if (ok && g > 0) ok = mbar_wait(bar(kBarChunkFree), 1, wc) && mbar_wait(bar(kBarChunkFree + 1), 1, wc);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int kb = 0; kb < 8; ++kb) {
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          umma_f16(tmem + kTmS, smem_desc_sw128(kv + kb * kBlk + ks * 32, 16, 1024),
+                   smem_desc_sw128(qb + 2 * kb * kBlk + ks * 32, 16, 1024), kIdescS, (kb | ks) != 0);
+      }
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        umma_f16(tmem + kTmS, smem_desc_sw128(kv + 8 * kBlk + ks * 32, 16, 1024),
+                 smem_desc_sw128(qb + 16 * kBlk + ks * 32, 16, 1024), kIdescSRope, 1);
+      umma_commit(bar(kBarS));
+      ok = mbar_wait(bar(kBarP), g & 1, wc);
+      if (ok && j == s.j0 && segs > 0) ok = mbar_wait(bar(kBarDqFree), (segs - 1) & 1, wc);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int mb = 0; mb < 5; ++mb) {
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          umma_f16(tmem + kTmDq + 64 * mb, smem_desc_sw128(kv + 2 * mb * kBlk + ks * 2048, kBlk, 1024),
+                   smem_desc_sw128(ds + ks * 2048, kBlk, 1024), mb < 4 ? kIdescDq : kIdescDqRope, j > s.j0 || ks > 0);
+      }
+      umma_commit(bar(kBarKvFree));
+#pragma unroll 1
+      for (int cb = 0; cb < 5; ++cb) {
+        // blocks go to the S^T, dP^T, third, S^T, dP^T columns; use n of a block waits for use n - 1
+        const int b = cb < 3 ? cb : cb - 3;
+        const uint32_t n = b == 2 ? g : 2 * g + (cb >= 3 ? 1 : 0);
+        if (cb >= 2 && n > 0) ok = mbar_wait(bar(kBarChunkFree + b), (n - 1) & 1, wc);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (b == 2 ? kTmX : kTmS + 64 * b);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          umma_f16(d, smem_desc_sw128(qb + 4 * cb * kBlk + ks * 2048, 2 * kBlk, 1024),
+                   smem_desc_sw128(ds + ks * 32, 16, 1024), cb < 4 ? kIdescKv : kIdescKvRope, ks > 0);
+        if (cb < 4) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_f16(d, smem_desc_sw128(qb + (4 * cb + 1) * kBlk + ks * 2048, 2 * kBlk, 1024),
+                     smem_desc_sw128(pb + ks * 32, 16, 1024), kIdescKv, 1);
+        }
+        umma_commit(bar(kBarChunk + b));
+      }
+    }
+    umma_commit(bar(kBarSeg));
+    umma_commit(bar(kBarDq));
+    ++segs;
+  }
+  umma_commit(bar(kBarDone));
+  mbar_wait_ignoring_abort(bar(kBarDone), 0, wc);  // nothing runs when tensor memory is released
+}
+
+__device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* smem, Misc* misc, uint32_t tmem,
+                                             uint32_t bars, const WaitCtl& wc) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quad = warp & 3, half = warp >> 2;
+  auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
+  // S^T (64 entries in lanes 0-15 of each quadrant): this thread's entry, and its heads 32 half +
+  // 2 i + odd
+  const int e = 16 * quad + (lane >> 2) + 8 * (lane & 1), odd = (lane >> 1) & 1;
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
+  const float scale_log2 = p.scale * kLog2e;
+  uint32_t g = 0, segs = 0;
+  SegIter it(p);
+  Seg s;
+  while (it.next(s)) {
+    const bool any = s.j0 < s.j1;
+    float lse2[16], delta[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = 32 * half + 2 * i + odd;
+      const float2 v = r < s.nvalid ? p.stats[s.base + r] : make_float2(CUDART_INF_F, 0.f);
+      lse2[i] = v.x;
+      delta[i] = v.y;
+    }
+    for (int j = s.j0; j < s.j1; ++j, ++g) {
+      mbar_wait(bar(kBarS), g & 1, wc);
+      tc_fence_after();
+      uint32_t sv[16], dv[16];
+      tmem_ld_16x64b_x16(lanes + kTmS + 32 * half, sv);
+      tmem_ld_16x64b_x16(lanes + kTmS + 64 + 32 * half, dv);
+      tmem_ld_wait();
+      const bool live = misc->slot[g & 3][e] >= 0;
+      float w = 0.f;
+      uint32_t pk[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float x = ex2_approx(fmaf(__uint_as_float(sv[i]), scale_log2, -lse2[i]));
+        const float pr = live ? x : 0.f;
+        const float d = live ? pr * (__uint_as_float(dv[i]) - delta[i]) * p.scale : 0.f;
+        w += pr;
+        pk[i] = pack_bf16x2(pr, d);
+      }
+      // neighbours hold the even and the odd heads of an entry: one shuffle each, and the even one
+      // writes the row of P, the odd one the row of dS
+      uint32_t out[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, pk[i], 2);
+        out[i] = odd ? __byte_perm(o, pk[i], 0x7632) : __byte_perm(pk[i], o, 0x5410);
+      }
+      uint8_t* dst = smem + (odd ? kOffDs : kOffP);
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        *reinterpret_cast<uint4*>(dst + sw128_offset(e, 4 * half + v)) =
+            make_uint4(out[4 * v], out[4 * v + 1], out[4 * v + 2], out[4 * v + 3]);
+      if (p.weights != nullptr) {
+        w += __shfl_xor_sync(0xffffffffu, w, 2);
+        if (half == 1 && !odd) misc->weight[e] = w;
+        named_bar_sync(1 + quad, 64);
+        const int k = j * kEntries + e;
+        if (half == 0 && !odd && live && k < p.K) {
+          float* dstw = p.weights + static_cast<long long>(s.t) * p.K + k;
+          // two head chunks add to a zero: the same sum in either order
+          if (p.hchunks > 1) atomicAdd(dstw, w + misc->weight[e]);
+          else *dstw = w + misc->weight[e];
+        }
+      }
+      fence_proxy_async_smem();  // P and dS -> MMA operand reads
+      tc_fence_before();
+      mbar_arrive(bar(kBarP));
+    }
+    // dq^T: lane = channel, this warp's heads 32 half .. + 31
+    if (any) {
+      mbar_wait(bar(kBarDq), segs & 1, wc);
+      tc_fence_after();
+    }
+#pragma unroll 1
+    for (int mb = 0; mb < 5; ++mb) {
+      uint32_t v[32];
+      if (any) {
+        tmem_ld32(lanes + kTmDq + 64 * mb + 32 * half, v);
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0u;
+      }
+      if (mb == 4 && lane >= 16) continue;
+      const int c = 128 * mb + (mb < 4 ? 32 : 16) * quad + lane;
+      if (s.whole) {
+        uint16_t* dst = p.dq + (s.base + 32 * half) * kRow + c;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (32 * half + i < s.nvalid) dst[i * kRow] = static_cast<uint16_t>(pack_bf16x2(__uint_as_float(v[i]), 0.f));
+      } else {
+        float* dst = p.dq_part + (static_cast<long long>(s.part) * kRows + 32 * half) * kRow + c;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (32 * half + i < s.nvalid) dst[i * kRow] = __uint_as_float(v[i]);
+      }
+    }
+    if (any) {
+      tc_fence_before();
+      mbar_arrive(bar(kBarDqFree));
+      ++segs;
+    }
+  }
+}
+
+__device__ __forceinline__ void scatter_role(const BackwardParams& p, Misc* misc, uint32_t tmem, uint32_t bars,
+                                             const WaitCtl& wc) {
+  const int warp = (threadIdx.x >> 5) - kScatWarp0, lane = threadIdx.x & 31;
+  const int quad = warp & 3;
+  const uint32_t group = static_cast<uint32_t>(warp >> 2);  // takes every second block
+  auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
+  uint32_t g = 0;
+  SegIter it(p);
+  Seg s;
+  while (it.next(s)) {
+    for (int j = s.j0; j < s.j1; ++j, ++g) {
+#pragma unroll 1
+      for (int cb = 0; cb < 5; ++cb) {
+        if (((5 * g + cb) & 1) != group) continue;
+        const int b = cb < 3 ? cb : cb - 3;
+        const uint32_t n = b == 2 ? g : 2 * g + (cb >= 3 ? 1 : 0);
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarChunk + b), n & 1, wc))) return;
+        tc_fence_after();
+        uint32_t v[2][32];
+        tmem_ld32(lanes + (b == 2 ? kTmX : kTmS + 64 * b), v[0]);
+        tmem_ld32(lanes + (b == 2 ? kTmX : kTmS + 64 * b) + 32, v[1]);
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(bar(kBarChunkFree + b));
+        if (cb == 4 && lane >= 16) continue;
+        float* dst = p.dkv_acc + 128 * cb + (cb < 4 ? 32 : 16) * quad + lane;
+        const int4* slots = reinterpret_cast<const int4*>(misc->slot[g & 3]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int4 sl = slots[i];
+          const int a[4] = {sl.x, sl.y, sl.z, sl.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (a[u] >= 0) atomicAdd(dst + static_cast<long long>(a[u]) * kRow, __uint_as_float(v[i >> 3][(4 * i + u) & 31]));
+        }
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) backward_kernel(const BackwardParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Misc* misc = reinterpret_cast<Misc*>(smem + kOffMisc);
+  const int warp = threadIdx.x >> 5;
+  const uint32_t bars = smem_u32(misc->bars);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNumBars; ++i) {
+      int count = 1;
+      if (i == kBarKvFull) count = kFillThreads;
+      if (i == kBarP || i == kBarDqFree) count = 32 * kSoftWarps;
+      if (i >= kBarChunkFree && i < kBarChunkFree + 3) count = 128;
+      mbar_init(bars + 8 * i, count);
+    }
+    misc->abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&misc->tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc->tmem;
+  const WaitCtl wc{p.status, &misc->abort_flag, p.wait_limit_ns ? p.wait_limit_ns : kWaitLimitNs};
+  if (warp < kScatWarp0) {
+    softmax_role(p, smem, misc, tmem, bars, wc);
+  } else if (warp < kFillWarp0) {
+    scatter_role(p, misc, tmem, bars, wc);
+  } else if (warp < kMmaWarp) {
+    gather_role(p, smem, misc, bars, wc);
+  } else if ((threadIdx.x & 31) == 0) {
+    mma_role(p, smem, tmem, bars, wc);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// One CTA per query: its list's cache rows and how far the live ones reach, and per head
+// (lse in log2 units, delta). A head without a live entry (lse = -inf) gets +inf: P = 0.
+constexpr int kPrepThreads = 256;
+__global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const BackwardParams p, const ListParams l) {
+  __shared__ int reach;
+  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  if (tid == 0) reach = 0;
+  __syncthreads();
+  const ReqContext ctx = request_context(t, l.req_of_token, l.block_table, l.num_reqs, l.max_blocks, l.seq_lens);
+  const int len = l.topk_len ? l.topk_len[t] : p.K;
+  int err = 0, last = 0;
+  for (int k = tid; k < p.K; k += kPrepThreads) {
+    const long long at = static_cast<long long>(t) * p.K + k;
+    int slot = -1;
+    if (k < len) {
+      const int pos = __ldg(l.topk + at);
+      slot = slot_of(pos, page_of(pos, ctx, l.max_blocks, l.page_size), ctx, l.block_table != nullptr, l.max_blocks,
+                     l.page_size, l.num_pages, &err);
+    }
+    p.slots[at] = slot;
+    if (p.weights != nullptr) p.weights[at] = 0.f;
+    if (slot >= 0) last = k + 1;
+  }
+  last = __reduce_max_sync(0xffffffffu, last);
+  if (lane == 0 && last > 0) atomicMax(&reach, last);
+  if (__any_sync(0xffffffffu, err != 0) && lane == 0) atomicOr(p.status, SVT_DEV_ERR_INDEX_RANGE);
+  for (int h = tid >> 5; h < p.H; h += kPrepThreads / 32) {
+    const long long r = static_cast<long long>(t) * p.H + h;
+    float d = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(p.out + r * kVdim) + lane + 32 * i);
+      const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.dout + r * kVdim) + lane + 32 * i);
+      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        d = fmaf(__uint_as_float(aw[k] << 16), __uint_as_float(bw[k] << 16), d);
+        d = fmaf(__uint_as_float(aw[k] & 0xFFFF0000u), __uint_as_float(bw[k] & 0xFFFF0000u), d);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if (lane == 0) {
+      const float lse = p.lse[r];
+      p.stats[r] = make_float2(lse == -CUDART_INF_F ? CUDART_INF_F : lse * kLog2e, d - (p.dlse ? p.dlse[r] : 0.f));
+    }
+  }
+  __syncthreads();
+  if (tid == 0) p.live_len[t] = reach;
+}
+
+// CTAs below join_ctas join the dq of the row-set that the border before CTA c + 1 of the main
+// kernel cuts (the first such border of the row-set does it), 8 rows each; the others round
+// the cache rows' sums to bf16, eight values at a time.
+constexpr int kJoinRows = 8;
+__global__ void __launch_bounds__(256) finish_kernel(const BackwardParams p, int join_ctas) {
+  if (static_cast<int>(blockIdx.x) < join_ctas) {
+    const int c = 1 + blockIdx.x / (kRows / kJoinRows), part0 = (blockIdx.x % (kRows / kJoinRows)) * kJoinRows;
+    const long long lo = streamk_lo(c, p.total_tiles, p.num_ctas);
+    const int r = static_cast<int>(lo / p.tiles);
+    const long long first = static_cast<long long>(r) * p.tiles;
+    if (lo == first || streamk_lo(c - 1, p.total_tiles, p.num_ctas) > first) return;
+    const int c1 = static_cast<int>(streamk_owner(first + p.tiles - 1, p.total_tiles, p.num_ctas));
+    const int t = r / p.hchunks, chunk = r - t * p.hchunks;
+    const int nvalid = min(kRows, p.H - chunk * kRows);
+    const long long base = static_cast<long long>(t) * p.H + chunk * kRows;
+    for (int i = threadIdx.x; i < kJoinRows * kRow; i += 256) {
+      const int row = part0 + i / kRow, col = i % kRow;
+      if (row >= nvalid) continue;
+      float sum = 0.f;
+      for (int k = c - 1; k <= c1; ++k) {
+        const long long slot = streamk_part_slot(k, first, p.total_tiles, p.num_ctas);
+        sum += p.dq_part[(slot * kRows + row) * kRow + col];
+      }
+      p.dq[(base + row) * kRow + col] = static_cast<uint16_t>(pack_bf16x2(sum, 0.f));
+    }
+    return;
+  }
+  const long long n8 = p.num_slots * (kRow / 8), step = (gridDim.x - join_ctas) * 256ll;
+  for (long long i = (blockIdx.x - join_ctas) * 256ll + threadIdx.x; i < n8; i += step) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p.dkv_acc) + 2 * i);
+    const float4 b = __ldcs(reinterpret_cast<const float4*>(p.dkv_acc) + 2 * i + 1);
+    reinterpret_cast<uint4*>(p.dkv)[i] = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w),
+                                                    pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
   }
 }
 
 }  // namespace
 
-cudaError_t launch_backward(const BackwardParams& p, cudaStream_t stream) {
-  const int tiles = (p.K + kTile - 1) / kTile;
-  cudaError_t e = cudaSuccess;
-  if (p.T > 0 && tiles > 0) {
-    backward_kernel<<<static_cast<unsigned>(static_cast<long long>(p.T) * tiles), kThreads, 0, stream>>>(p);
+void plan_backward(BackwardParams& p, int sms) {
+  p.hchunks = (p.H + kRows - 1) / kRows;
+  p.tiles = (p.K + kEntries - 1) / kEntries;
+  p.total_tiles = static_cast<long long>(p.T) * p.hchunks * p.tiles;
+  p.num_ctas = static_cast<int>(p.total_tiles < sms ? p.total_tiles : sms);
+}
+
+cudaError_t launch_backward(const BackwardParams& p, const ListParams& l, cudaStream_t stream) {
+  cudaError_t e = cudaMemsetAsync(p.dkv_acc, 0, static_cast<size_t>(p.num_slots) * kRow * sizeof(float), stream);
+  if (e != cudaSuccess) return e;
+  int join = 0;
+  if (p.total_tiles > 0) {
+    e = cudaFuncSetAttribute(backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    prepare_kernel<<<static_cast<unsigned>(p.T), kPrepThreads, 0, stream>>>(p, l);
     e = cudaGetLastError();
-  }
-  const long long nq = static_cast<long long>(p.T) * p.H * (kRow / 8), nk = p.num_slots * (kRow / 8);
-  if (e == cudaSuccess && nq > 0) {
-    round_kernel<<<static_cast<unsigned>(nq / 256 + 1 < 1216 ? nq / 256 + 1 : 1216), 256, 0, stream>>>(p.dq_acc, p.dq, nq);
+    if (e != cudaSuccess) return e;
+    backward_kernel<<<static_cast<unsigned>(p.num_ctas), kThreads, kSmem, stream>>>(p);
     e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    join = (p.num_ctas - 1) * (kRows / kJoinRows);
+  } else if (p.T > 0) {
+    e = cudaMemsetAsync(p.dq, 0, static_cast<size_t>(p.T) * p.H * kRow * sizeof(uint16_t), stream);
+    if (e != cudaSuccess) return e;
   }
-  if (e == cudaSuccess) {
-    round_kernel<<<static_cast<unsigned>(nk / 256 + 1 < 1216 ? nk / 256 + 1 : 1216), 256, 0, stream>>>(p.dkv_acc, p.dkv, nk);
-    e = cudaGetLastError();
-  }
-  return e;
+  const long long n = (p.num_slots * (kRow / 8) + 255) / 256;
+  finish_kernel<<<static_cast<unsigned>(join + (n < 1216 ? n : 1216)), 256, 0, stream>>>(p, join);
+  return cudaGetLastError();
 }
 
 }  // namespace svt

@@ -258,15 +258,36 @@ struct BackwardParams {
   long long row_stride, num_slots;
   int T, H, K;
   float scale;
-  const int32_t* slots;  // [T, K] resolved, -1 = dead
-  uint16_t* dq;          // [T, H, 576]
-  uint16_t* dkv;         // [num_slots, 576]
-  float* weights;        // [T, K] or null
-  float* dkv_acc;        // [num_slots, 576], zero on entry
-  float* dq_acc;         // [T, H, 576], zero on entry
+  uint16_t* dq;    // [T, H, 576]
+  uint16_t* dkv;   // [num_slots, 576]
+  float* weights;  // [T, K] or null
+  // scratch
+  int32_t* slots;     // [T, K] resolved, -1 = dead
+  int32_t* live_len;  // [T] entries up to the last live one
+  float2* stats;      // [T, H]: lse in log2 units (+inf for a head with no live entry), delta
+  float* dq_part;     // [2 * num_ctas, 64, 576]: dq of row-sets cut between CTAs
+  float* dkv_acc;     // [num_slots, 576]
   int* status;
+  unsigned long long wait_limit_ns;  // 0 = the default
+  int fault;                         // planted faults (kFault* bits)
+  // schedule (plan_backward): 64-head chunks per query, 64-entry tiles per row-set
+  int hchunks, tiles, num_ctas;
+  long long total_tiles;
 };
-cudaError_t launch_backward(const BackwardParams& p, cudaStream_t stream);
+// How the lists resolve to cache rows.
+struct ListParams {
+  const int32_t* topk;
+  const int32_t* topk_len;
+  const int32_t* req_of_token;
+  const int32_t* block_table;
+  int num_reqs, max_blocks;
+  const int32_t* seq_lens;
+  int page_size;
+  long long num_pages;
+};
+// Fills the schedule fields from T, H and K for `sms` SMs.
+void plan_backward(BackwardParams& p, int sms);
+cudaError_t launch_backward(const BackwardParams& p, const ListParams& lists, cudaStream_t stream);
 
 // The checks of a cache descriptor (and its row stride) and of a workspace that every entry point makes.
 svt_status check_kv_cache(const svt_kv_cache* kv, long long* row_stride);

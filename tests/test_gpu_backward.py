@@ -215,6 +215,17 @@ def test_backward_matches_differences_of_the_forward(S):
     assert abs(num - ana) <= slack + moved * reach + 1e-6 * (abs(num) + 1)
 
 
+def test_backward_is_repeatable_but_for_the_cache_sums(S):
+    q, cache, dout = normal(40, 50, 16, 576).cuda(), normal(41, 500, 576).cuda(), normal(42, 50, 16, 512).cuda()
+    slots = lists(43, 50, 300, 500).cuda()
+    kv = S.KVCache(cache, 500, 1, W.KV_BF16)
+    out, lse = forward(S, q, kv, slots)
+    ws = S.Workspace()
+    a = S.sparse_mla_backward(q, kv, slots, SCALE, out, lse, dout, return_weights=True, ws=ws)
+    b = S.sparse_mla_backward(q, kv, slots, SCALE, out, lse, dout, return_weights=True, ws=ws)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[2], b[2])
+
+
 def test_backward_in_graphs_and_on_two_streams(S):
     """Two captured graphs with a workspace each, replayed on two streams at once, on inputs that changed
     after the capture, against eager calls."""
