@@ -500,15 +500,23 @@ __global__ void __launch_bounds__(256) finish_kernel(const BackwardParams p, int
     const int t = r / p.hchunks, chunk = r - t * p.hchunks;
     const int nvalid = min(kRows, p.H - chunk * kRows);
     const long long base = static_cast<long long>(t) * p.H + chunk * kRows;
-    for (int i = threadIdx.x; i < kJoinRows * kRow; i += 256) {
-      const int row = part0 + i / kRow, col = i % kRow;
-      if (row >= nvalid) continue;
-      float sum = 0.f;
-      for (int k = c - 1; k <= c1; ++k) {
-        const long long slot = streamk_part_slot(k, first, p.total_tiles, p.num_ctas);
-        sum += p.dq_part[(slot * kRows + row) * kRow + col];
+    // CTA c - 1's part may be its second; every later one begins inside the row-set: its first
+    const float* a = p.dq_part + streamk_part_slot(c - 1, first, p.total_tiles, p.num_ctas) * (kRows * kRow);
+    const float* b = p.dq_part + 2ll * c * (kRows * kRow);
+    const int more = c1 - c + 1;
+    for (int i = threadIdx.x; i < kJoinRows * (kRow / 4); i += 256) {
+      const int row = part0 + i / (kRow / 4), at = row * kRow + 4 * (i % (kRow / 4));
+      if (row >= nvalid) break;
+      float4 sum = *reinterpret_cast<const float4*>(a + at);
+#pragma unroll 4
+      for (int k = 0; k < more; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(b + at + 2ll * k * (kRows * kRow));
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
       }
-      p.dq[(base + row) * kRow + col] = static_cast<uint16_t>(pack_bf16x2(sum, 0.f));
+      *reinterpret_cast<uint2*>(p.dq + base * kRow + at) = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
     }
     return;
   }

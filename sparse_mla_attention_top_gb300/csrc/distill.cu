@@ -4,14 +4,16 @@
 //   q = softmax(x / tau) over all candidates, or over the listed ones,
 //   loss = sum_j p_j (ln p_j - ln q_j),   d loss / d x_n = (q_n - sum of p at n) / tau.
 // With W = sum w, A = sum w ln w, B = sum w x / tau and the student's normaliser lse (natural
-// log): loss = A / W - ln W - B / W + lse, so one sweep over the list serves the loss.
+// log): loss = A / W - ln W - B / W + lse, so one sweep over the list serves the loss. Everything
+// runs in log2 units, exponents relative to the row's largest score.
 //
 // Bound: reading the scores once and writing the gradient once. A row is cut between the CTAs
 // of a cluster so that each part (up to 64 KB) stays in shared memory: it is read from memory
 // once, turned into exp(x - max) in place (one exponential per score for loss and gradient),
-// and after the cluster has exchanged (max, sum, B) scaled, corrected at the listed positions
-// and written. Three CTAs of 512 threads share an SM, so one's reads overlap another's writes.
-// Rows longer than eight parts are swept twice from memory.
+// and after the cluster has exchanged its sums scaled on the way out; the listed columns are
+// put right behind it. A list of up to 2048 entries stays in registers, and the CTAs of a row share
+// out its sums. Three CTAs of 512 threads share an SM, so one's reads overlap another's writes.
+// Longer lists, and rows of more than eight parts, are read again where they are needed.
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
@@ -31,29 +33,35 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxSplit = 8;
 
 struct Stats {
-  float m, s, b;  // running max (log2 units), sum of 2^(x - m), sum of w x (log2 units)
+  float m, s;     // largest score, sum of 2^(c (x - m)) (this CTA's candidates)
+  float w, a, b;  // sums of w, w log2 w and w c x (this CTA's share of the list)
 };
 
 struct DistillShared {
-  float red[kWarps];
+  float4 red[2][kWarps];   // one array per reduction, in turns
   Stats stats[kMaxSplit];  // every CTA's, pushed by each
 };
 
-__device__ __forceinline__ float block_reduce(float v, bool is_max, float* red) {
+// Four values over the block: sums, or with kMax maxima. One barrier; `red` alternates between
+// calls, so that a slow warp still reads the previous array.
+template <bool kMax>
+__device__ __forceinline__ float4 block_reduce(float4 v, float4* red) {
+  auto op = [](float x, float y) { return kMax ? fmaxf(x, y) : x + y; };
+  auto step = [&](int o) {
+    v.x = op(v.x, __shfl_xor_sync(0xffffffffu, v.x, o));
+    v.y = op(v.y, __shfl_xor_sync(0xffffffffu, v.y, o));
+    if (!kMax) {
+      v.z = op(v.z, __shfl_xor_sync(0xffffffffu, v.z, o));
+      v.w = op(v.w, __shfl_xor_sync(0xffffffffu, v.w, o));
+    }
+  };
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float w = __shfl_xor_sync(0xffffffffu, v, o);
-    v = is_max ? fmaxf(v, w) : v + w;
-  }
-  __syncthreads();  // red is free
+  for (int o = 16; o > 0; o >>= 1) step(o);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   v = red[threadIdx.x & (kWarps - 1)];
 #pragma unroll
-  for (int o = kWarps / 2; o > 0; o >>= 1) {
-    const float w = __shfl_xor_sync(0xffffffffu, v, o);
-    v = is_max ? fmaxf(v, w) : v + w;
-  }
+  for (int o = kWarps / 2; o > 0; o >>= 1) step(o);
   return v;
 }
 
@@ -77,9 +85,9 @@ __device__ __forceinline__ void store4(uint16_t* p, float4 v) {
   __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)));
 }
 
-// Scores [a, a + n) times c into part[]; returns this thread's largest.
+// Scores [a, a + n) into part[]; returns this thread's largest.
 template <typename E>
-__device__ __forceinline__ float fill_part(const E* row, int a, int n, float c, bool vec, float* part) {
+__device__ __forceinline__ float fill_part(const E* row, int a, int n, bool vec, float* part) {
   float mx = -CUDART_INF_F;
   int j0 = 0;
   if (vec) {
@@ -92,10 +100,6 @@ __device__ __forceinline__ float fill_part(const E* row, int a, int n, float c, 
 #pragma unroll
       for (int u = 0; u < 4; ++u)
         if (j + u * kThreads < n4) {
-          v[u].x *= c;
-          v[u].y *= c;
-          v[u].z *= c;
-          v[u].w *= c;
           mx = fmaxf(fmaxf(mx, fmaxf(v[u].x, v[u].y)), fmaxf(v[u].z, v[u].w));
           reinterpret_cast<float4*>(part)[j + u * kThreads] = v[u];
         }
@@ -104,19 +108,64 @@ __device__ __forceinline__ float fill_part(const E* row, int a, int n, float c, 
   }
 #pragma unroll 8
   for (int j = j0 + threadIdx.x; j < n; j += kThreads) {
-    const float v = load1(row + a + j) * c;
+    const float v = load1(row + a + j);
     mx = fmaxf(mx, v);
     part[j] = v;
   }
   return mx;
 }
 
-// kAll: the softmax runs over all candidates, else over the listed ones.
-template <typename E, bool kAll>
+// This thread's sum of 2^(c x - base) over part[0 .. n), which are left in place of x with kKeep.
+// The exponent is one fma: its error is relative to c (x - max), small where the terms are large.
+template <bool kKeep>
+__device__ __forceinline__ float exp_part(float* part, int n, float c, float base) {
+  float s = 0.f;
+  const int n4 = n / 4;
+#pragma unroll 4
+  for (int j = threadIdx.x; j < n4; j += kThreads) {
+    float4 v = reinterpret_cast<float4*>(part)[j];
+    v.x = ex2_approx(fmaf(v.x, c, -base));
+    v.y = ex2_approx(fmaf(v.y, c, -base));
+    v.z = ex2_approx(fmaf(v.z, c, -base));
+    v.w = ex2_approx(fmaf(v.w, c, -base));
+    s += (v.x + v.y) + (v.z + v.w);
+    if (kKeep) reinterpret_cast<float4*>(part)[j] = v;
+  }
+  for (int j = 4 * n4 + threadIdx.x; j < n; j += kThreads) {
+    const float v = ex2_approx(fmaf(part[j], c, -base));
+    s += v;
+    if (kKeep) part[j] = v;
+  }
+  return s;
+}
+
+// part[0 .. n) times f to out.
+template <typename E>
+__device__ __forceinline__ void write_part(const float* part, int n, float f, bool vec, E* out) {
+  int j0 = 0;
+  if (vec) {
+    const int n4 = n / 4;
+#pragma unroll 4
+    for (int j = threadIdx.x; j < n4; j += kThreads) {
+      const float4 v = reinterpret_cast<const float4*>(part)[j];
+      store4(out + 4 * j, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+    }
+    j0 = 4 * n4;
+  }
+  for (int j = j0 + threadIdx.x; j < n; j += kThreads) store1(out + j, part[j] * f);
+}
+
+constexpr int kHeld = 4;  // list entries a thread keeps in registers: lists of up to 2048
+
+// kAll: the softmax runs over all candidates, else over the listed ones. kFit: the list is held in
+// registers and this CTA's columns in shared memory; otherwise both are read again where needed.
+template <typename E, bool kAll, bool kFit>
 __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParams p) {
   extern __shared__ float4 dyn[];
   float* part = reinterpret_cast<float*>(dyn);
   __shared__ DistillShared sh;
+  auto cl = cooperative_groups::this_cluster();
+  if (p.split > 1) cl.barrier_arrive();  // (completed below) every CTA of the cluster has started
   const int tid = threadIdx.x;
   const int t = blockIdx.x / p.split, cr = blockIdx.x - t * p.split;
   const E* row = static_cast<const E*>(p.scores) + static_cast<long long>(t) * p.stride;
@@ -128,152 +177,193 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
   // this CTA's candidates lo .. chi - 1
   const int share = ((len + p.split - 1) / p.split + 7) & ~7;
   const int lo = min(len, cr * share), chi = min(len, lo + share);
+  const int n = chi - lo;
   const bool vec = p.vec != 0;
   const float c = p.inv_tau * kLog2e;
 
-  // the teacher's list: every CTA of the row takes the whole list's sums (it is short), and the
-  // entries inside its own columns for B. Logits become weights 2^(c (value - max)).
-  float tmax = 0.f;
-  if (p.logits) {
-    tmax = -CUDART_INF_F;
-    for (int j = tid; j < p.K; j += kThreads) {
-      const int i = __ldg(idx + j);
-      if (i >= 0 && i < len) tmax = fmaxf(tmax, __ldg(val + j));
+  int held_i[kHeld];
+  float held_v[kHeld];
+  if constexpr (kFit) {
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const int j = tid + u * kThreads;
+      held_i[u] = j < p.K ? __ldg(idx + j) : -1;
+      held_v[u] = j < p.K ? __ldg(val + j) : 0.f;
     }
-    tmax = block_reduce(tmax, true, sh.red);
-    if (tmax == -CUDART_INF_F) tmax = 0.f;  // nothing listed: every weight below is 0
   }
-  auto weight = [&](int j, int i) -> float {
-    if (i < 0 || i >= len) return 0.f;
-    const float v = __ldg(val + j);
-    return p.logits ? exp2f((v - tmax) * c) : v;
+  // f(j, position, value) for the live entries of the list
+  auto entries = [&](auto f) {
+    if constexpr (kFit) {
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u)
+        if (held_i[u] >= 0 && held_i[u] < len) f(u, held_i[u], held_v[u]);
+    } else {
+      for (int j = tid; j < p.K; j += kThreads) {
+        const int i = __ldg(idx + j);
+        if (i >= 0 && i < len) f(j / kThreads, i, __ldg(val + j));
+      }
+    }
   };
-  float W = 0.f, A = 0.f;
-  Stats st{-CUDART_INF_F, 0.f, 0.f};
-  for (int j = tid; j < p.K; j += kThreads) {
-    const int i = __ldg(idx + j);
-    const float w = weight(j, i);
-    W += w;
-    if (w != 0.f) {
-      A += p.logits ? w * ((__ldg(val + j) - tmax) * c) : w * log2f(w);
-      if (i >= lo && i < chi) st.b += w * (load1(row + i) * c);
-    }
-    if (!kAll && i >= 0 && i < len) st.m = fmaxf(st.m, load1(row + i) * c);
-  }
-  W = block_reduce(W, false, sh.red);
-  A = block_reduce(A, false, sh.red);
-  st.b = block_reduce(st.b, false, sh.red);
 
-  const int n = chi - lo;
-  const bool resident = kAll && n <= kPart;
+  // largest candidate (or listed score) and largest teacher value
+  float mx = -CUDART_INF_F, tmax = -CUDART_INF_F;
   if constexpr (kAll) {
+    if (kFit) mx = fill_part(row, lo, n, vec, part);
+  } else {
+    if (kFit)
+      for (int j = tid; j < n; j += kThreads) part[j] = 0.f;
+  }
+  Stats st{-CUDART_INF_F, 0.f, 0.f, 0.f, 0.f};
+  if constexpr (kAll && !kFit) {
     for (int a = lo; a < chi; a += kPart) {
       const int m = min(kPart, chi - a);
-      const float mx = block_reduce(fill_part(row, a, m, c, vec, part), true, sh.red);
-      const float nm = fmaxf(st.m, mx);
-      const float base = nm == -CUDART_INF_F ? 0.f : nm;
-      float s = 0.f;
-      const int m4 = m / 4;
-      for (int j = tid; j < m4; j += kThreads) {
-        float4 v = reinterpret_cast<float4*>(part)[j];
-        v.x = ex2_approx(v.x - base);
-        v.y = ex2_approx(v.y - base);
-        v.z = ex2_approx(v.z - base);
-        v.w = ex2_approx(v.w - base);
-        s += (v.x + v.y) + (v.z + v.w);
-        if (resident) reinterpret_cast<float4*>(part)[j] = v;
-      }
-      for (int j = 4 * m4 + tid; j < m; j += kThreads) {
-        const float v = ex2_approx(part[j] - base);
-        s += v;
-        if (resident) part[j] = v;
-      }
-      s = block_reduce(s, false, sh.red);
-      st.s = (st.m == -CUDART_INF_F ? 0.f : st.s * exp2f(st.m - base)) + s;
+      const float nm = fmaxf(st.m, block_reduce<true>(make_float4(fill_part(row, a, m, vec, part), 0.f, 0.f, 0.f), sh.red[0]).x);
+      const float s = block_reduce<false>(
+          make_float4(exp_part<false>(part, m, c, nm == -CUDART_INF_F ? 0.f : __fmul_rn(nm, c)), 0.f, 0.f, 0.f), sh.red[1]).x;
+      st.s = (st.m == -CUDART_INF_F ? 0.f : st.s * exp2f(__fmul_rn(st.m, c) - __fmul_rn(nm, c))) + s;
       st.m = nm;
     }
-  } else {
-    // the listed scores only; every CTA takes the whole list
-    st.m = block_reduce(st.m, true, sh.red);
-    const float base = st.m == -CUDART_INF_F ? 0.f : st.m;
-    for (int j = tid; j < p.K; j += kThreads) {
-      const int i = __ldg(idx + j);
-      if (i >= 0 && i < len) st.s += exp2f(load1(row + i) * c - base);
+    mx = st.m;
+  }
+  entries([&](int, int i, float v) {
+    if (!kAll) mx = fmaxf(mx, load1(row + i));
+    tmax = fmaxf(tmax, v);
+  });
+  {
+    const float4 r = block_reduce<true>(make_float4(mx, tmax, 0.f, 0.f), sh.red[0]);
+    st.m = r.x;
+    tmax = r.y == -CUDART_INF_F ? 0.f : r.y;  // nothing listed: every weight is 0
+  }
+  // logits become weights 2^(c (value - max))
+  auto weight = [&](float v) { return p.logits ? exp2f((v - tmax) * c) : v; };
+  float base = st.m == -CUDART_INF_F ? 0.f : __fmul_rn(st.m, c);
+  {
+    // a CTA takes every split-th entry for the sums of the list (each entry of a listed softmax)
+    float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (kAll && kFit) r.x = exp_part<true>(part, n, c, base);
+    entries([&](int u, int i, float v) {
+      const bool mine = ((tid + u * kThreads) & (p.split - 1)) == cr;
+      if (kAll && !mine) return;
+      const float x = load1(row + i);
+      if (!kAll) r.x += exp2f(fmaf(x, c, -base));
+      if (!mine) return;
+      const float w = weight(v);
+      r.y += w;
+      if (w != 0.f) {
+        r.z += p.logits ? w * ((v - tmax) * c) : w * log2f(w);
+        r.w += w * (x * c);
+      }
+    });
+    r = block_reduce<false>(r, sh.red[1]);
+    if (!(kAll && !kFit)) st.s = r.x;
+    st.w = r.y;
+    st.a = r.z;
+    st.b = r.w;
+  }
+  // the listed columns of this CTA as they stand, before any of them changes
+  float held_e[kHeld];
+  if constexpr (kAll && kFit) {
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      held_e[u] = 0.f;
+      if (held_i[u] >= lo && held_i[u] < chi) held_e[u] = part[held_i[u] - lo];
     }
-    st.s = block_reduce(st.s, false, sh.red);
   }
 
-  float M = st.m, Z = st.s, B = st.b;
+  float M = st.m, Z = st.s, W = st.w, A = st.a, B = st.b;
   if (p.split > 1) {
-    auto cl = cooperative_groups::this_cluster();
-    cl.sync();  // every CTA of the cluster has started
+    cl.barrier_wait();
     if (tid < p.split) cl.map_shared_rank(&sh, static_cast<unsigned>(tid))->stats[cr] = st;
     cl.sync();  // every CTA's statistics are here
-    B = 0.f;
-    for (int r = 0; r < p.split; ++r) B += sh.stats[r].b;
+    W = A = B = 0.f;
+    for (int r = 0; r < p.split; ++r) {
+      W += sh.stats[r].w;
+      A += sh.stats[r].a;
+      B += sh.stats[r].b;
+    }
     if constexpr (kAll) {
       M = -CUDART_INF_F;
       for (int r = 0; r < p.split; ++r) M = fmaxf(M, sh.stats[r].m);
       Z = 0.f;
-      for (int r = 0; r < p.split; ++r)
-        if (sh.stats[r].m != -CUDART_INF_F) Z += sh.stats[r].s * exp2f(sh.stats[r].m - M);
-        else if (sh.stats[r].s != sh.stats[r].s) Z = sh.stats[r].s;  // a NaN score
+      for (int r = 0; r < p.split; ++r) {
+        const Stats q = sh.stats[r];
+        if (q.m != -CUDART_INF_F) Z += q.s * exp2f(__fmul_rn(q.m, c) - __fmul_rn(M, c));
+        else if (q.s != q.s) Z = q.s;  // NaN scores
+      }
     }
+  } else {
+    __syncthreads();  // every thread has read its listed columns
   }
+  const float top = M == -CUDART_INF_F ? 0.f : __fmul_rn(M, c);  // Z is relative to it
   // a row without a target, or whose candidates are all -inf, has loss 0 and gradient 0
   const bool some = !(W == 0.f) && !(M == -CUDART_INF_F && !(Z != Z));
   if (p.loss != nullptr && cr == 0 && tid == 0) {
-    // the four terms cancel to a small difference: joined in fp64
-    const double d = static_cast<double>(A) / W - static_cast<double>(B) / W + static_cast<double>(M) -
-                     log2(static_cast<double>(W)) + log2(static_cast<double>(Z));
+    // the terms cancel to a small difference: joined in fp64, of which there is one thread's worth (a
+    // logarithm in fp64 would hold the CTA up for microseconds: the fp32 one of the mantissa is as
+    // good next to an exact exponent)
+    int ez, ew;
+    const float mz = frexpf(Z, &ez), mw = frexpf(W, &ew);
+    double inv = static_cast<double>(1.f / W);
+    if (W > 1e-30f && W < 1e30f) inv = inv * (2.0 - W * inv);
+    else inv = 1.0 / W;
+    const double d = (static_cast<double>(A) - static_cast<double>(B)) * inv + static_cast<double>(top) +
+                     static_cast<double>(ez - ew) + (static_cast<double>(log2f(mz)) - static_cast<double>(log2f(mw)));
     p.loss[t] = some ? static_cast<float>(d * 0.69314718055994530942) : 0.f;
   }
   if (drow == nullptr) return;
 
-  const float g = (p.row_weight ? p.row_weight[t] : 1.f) * p.inv_tau;
-const int tail = ((p.N - len + p.split - 1) / p.split + 7) & ~7;  // this CTA's share of the columns behind
-  const int tlo = min(p.N, len + cr * tail), hi = min(p.N, tlo + tail);
-  const float gw = some ? -g / W : 0.f;
-  const float base = M == -CUDART_INF_F ? 0.f : M;
-  // resident parts hold 2^(x - the CTA's max); parts swept again hold x
-  const float scale = some ? (resident ? g / Z * (st.m == -CUDART_INF_F ? 0.f : exp2f(st.m - base)) : g / Z) : 0.f;
-  for (int a = lo; a < chi; a += kPart) {
-    const int m = min(kPart, chi - a);
-    __syncthreads();  // the part is free
-    if (!resident) {
-      if constexpr (kAll) {
-        fill_part(row, a, m, c, vec, part);
-      } else {
-        for (int j = tid; j < m; j += kThreads) part[j] = 0.f;
-      }
-      __syncthreads();
-    }
-    if constexpr (kAll) {
-      for (int j = tid; j < m; j += kThreads) {
-        const float e = resident ? part[j] : ex2_approx(part[j] - base);
-        part[j] = some ? e * scale : 0.f;
-      }
-      __syncthreads();
-    }
-    if (some) {
-      for (int j = tid; j < p.K; j += kThreads) {
-        const int i = __ldg(idx + j);
-        if (i < a || i >= a + m) continue;
-        float d = weight(j, i) * gw;
-        if constexpr (!kAll) d += exp2f(load1(row + i) * c - base) * scale;
-        if (d != 0.f) atomicAdd(part + (i - a), d);
-      }
-    }
+  const float g = some ? (p.row_weight ? p.row_weight[t] : 1.f) * p.inv_tau : 0.f;
+  const float gq = some ? g / Z : 0.f, gw = some ? -g / W : 0.f;
+  if constexpr (kAll && kFit) {
+    // part holds 2^(c x - base) of this CTA. A listed column is set to q's share, then p's are added (as
+    // often as it is listed); the sweep writes q's share everywhere, and the listed columns again
+    const float scale = some ? gq * exp2f(base - top) : 0.f;
+    auto mine = [&](int u) { return held_i[u] >= lo && held_i[u] < chi; };
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u)
+      if (mine(u)) part[held_i[u] - lo] = some ? held_e[u] * scale : 0.f;
     __syncthreads();
-    int j0 = 0;
-    if (vec) {
-      const int m4 = m / 4;
-      for (int j = tid; j < m4; j += kThreads) store4(drow + a + 4 * j, reinterpret_cast<float4*>(part)[j]);
-      j0 = 4 * m4;
+    if (some) {
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u)
+        if (mine(u)) atomicAdd(part + (held_i[u] - lo), weight(held_v[u]) * gw);
+      write_part(part, n, scale, vec, drow + lo);
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u)
+        if (mine(u)) store1(drow + held_i[u], part[held_i[u] - lo]);
+    } else {
+      for (int j = tid; j < n; j += kThreads) store1(drow + lo + j, 0.f);
     }
-    for (int j = j0 + tid; j < m; j += kThreads) store1(drow + a + j, part[j]);
+  } else {
+    for (int a = lo; a < chi; a += kPart) {
+      const int m = min(kPart, chi - a);
+      if constexpr (kAll) {
+        __syncthreads();
+        fill_part(row, a, m, vec, part);
+        __syncthreads();
+        for (int j = tid; j < m; j += kThreads) part[j] = some ? ex2_approx(fmaf(part[j], c, -top)) * gq : 0.f;
+        __syncthreads();
+      } else if constexpr (!kFit) {
+        __syncthreads();
+        for (int j = tid; j < m; j += kThreads) part[j] = 0.f;
+        __syncthreads();
+      }
+      if (some) {
+        entries([&](int, int i, float v) {
+          if (i < a || i >= a + m) return;
+          float d = weight(v) * gw;
+          if (!kAll) d += exp2f(fmaf(load1(row + i), c, -top)) * gq;
+          if (d != 0.f) atomicAdd(part + (i - a), d);
+        });
+      }
+      __syncthreads();
+      write_part(part, m, 1.f, vec, drow + a);
+    }
   }
-  // columns behind the candidates
+  // this CTA's share of the columns behind the candidates
+  const int tail = ((p.N - len + p.split - 1) / p.split + 7) & ~7;
+  const int tlo = min(p.N, len + cr * tail), hi = min(p.N, tlo + tail);
   int j = tlo;
   if (vec) {
     const int al = min(hi, (tlo + 3) & ~3);
@@ -298,10 +388,11 @@ cudaError_t launch_e(DistillParams p, cudaStream_t stream) {
                                (static_cast<long long>(p.T) * split < 2ll * sms && p.N / (2 * split) >= 2048)))
     split *= 2;
   p.split = split;
-  const int per = (p.N + split - 1) / split + 8;
-  const size_t smem = static_cast<size_t>(per < kPart ? (per + 3) & ~3 : kPart) * sizeof(float);
-  e = cudaFuncSetAttribute(distill_kernel<E, kAll>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(kPart * sizeof(float)));
+  const int per = ((p.N + split - 1) / split + 7) & ~7;  // the largest part (the kernel's share for len = N)
+  const size_t smem = static_cast<size_t>(per < kPart ? per : kPart) * sizeof(float);
+  const bool fit = p.K <= kHeld * kThreads && per <= kPart;
+  const auto kernel = fit ? distill_kernel<E, kAll, true> : distill_kernel<E, kAll, false>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPart * sizeof(float)));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.T) * split));
@@ -315,7 +406,7 @@ cudaError_t launch_e(DistillParams p, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, distill_kernel<E, kAll>, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace

@@ -312,38 +312,54 @@ def topk_select(scores, K: int, *, lens=None, out=None):
     return out
 
 
-def _on_device(device, **tensors) -> None:
-    """Every given tensor is on `device`, which is the current CUDA device (kernels are launched
-    there, on its current stream)."""
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise TypeError(f"tensors must be on the current CUDA device, not {device}")
+# The current stream's handle without building a Stream object (several microseconds a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch_on(first, **tensors):
+    """The device index and current stream of a launch: `first` is on the current CUDA device
+    (kernels are launched there, on its current stream) and every other given tensor beside it."""
+    dev = first.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise TypeError(f"tensors must be on the current CUDA device, not {first.device}")
     for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise TypeError(f"{name} must be on {device}, not {t.device}")
+        if t is not None and t.get_device() != dev:
+            raise TypeError(f"{name} must be on {first.device}, not {t.device}")
+    return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(dev)
 
 
 def _shaped(t, name: str, dtype, shape):
-    """`t`, when it is None or a contiguous tensor of this type and shape."""
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+    """The address of `t`, a contiguous tensor of this type and shape; None for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
-    return t
+    return t.data_ptr()
 
 
 def _choice(value: str, choices: dict, name: str) -> int:
-    if value not in choices:
+    code = choices.get(value)
+    if code is None:
         raise ValueError(f"{name} must be one of {', '.join(choices)}, got {value!r}")
-    return choices[value]
+    return code
 
 
 def _rows3(x, name: str):
     """x [T, D] or [T, H, D] as (T, H, D, stride t, stride h); unit column stride. A dimension of
     one row has no meaningful stride."""
-    if x.dim() not in (2, 3) or (x.shape[-1] > 1 and x.stride(-1) != 1):
-        raise TypeError(f"{name} must be [T, D] or [T, H, D] with unit column stride")
-    T, H, D = (x.shape[0], 1, x.shape[1]) if x.dim() == 2 else x.shape
-    sh = D if x.dim() == 2 or H <= 1 else x.stride(1)
-    st = H * D if T <= 1 else x.stride(0)
-    return T, H, D, st, sh
+    shape, stride = x.shape, x.stride()
+    if len(shape) == 3:
+        T, H, D = shape
+        st, sh, sd = stride
+    elif len(shape) == 2:
+        T, D = shape
+        st, sd = stride
+        H, sh = 1, D
+    else:
+        raise TypeError(f"{name} must be [T, D] or [T, H, D]")
+    if sd != 1 and D > 1:
+        raise TypeError(f"{name} must have unit column stride")
+    return T, H, D, (st if T > 1 else H * D), (sh if H > 1 else D)
 
 
 def rope_frequencies(dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
@@ -357,31 +373,26 @@ def rope_frequencies(dim: int, base: float = 10000.0, *, scaling: str = "none", 
     return host.to(torch.device("cuda", torch.cuda.current_device()) if device is None else device)
 
 
-def _freqs(freqs):
-    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
-        raise TypeError("freqs must be a contiguous fp64 [dim / 2] tensor")
-    return freqs
-
-
 def rope(x, positions, freqs, *, offset: int = 0, layout: str = "interleaved", inverse: bool = False,
          amplitude: float = 1.0, out=None):
     """svt_rope: rotates columns offset .. offset + 2 len(freqs) - 1 of x ([T, H, D] or [T, D], bf16
     or fp32, rows may be strided) by its tokens' positions; the other columns are copied. out=x
     rotates in place. inverse=True turns back: it maps the gradient of the result to x's."""
-    if x.dtype not in (torch.bfloat16, torch.float32):
+    dtype = x.dtype
+    if dtype != torch.bfloat16 and dtype != torch.float32:
         raise TypeError("x must be bf16 or fp32")
     T, H, D, xt, xh = _rows3(x, "x")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if out.dtype != x.dtype or out.shape != x.shape:
+        out = torch.empty(x.shape, dtype=dtype, device=x.device)
+    elif out.dtype != dtype or out.shape != x.shape:
         raise TypeError("out must have x's type and shape")
     _, _, _, ot, oh = _rows3(out, "out")
-    dim = 2 * _freqs(freqs).numel()
-    _shaped(_i32(positions, "positions"), "positions", torch.int32, (T,))
-    _on_device(x.device, positions=positions, freqs=freqs, out=out)
-    _check(lib().svt_rope(_ptr(x), _ptr(out), 1 if x.dtype == torch.float32 else 0, T, H, D, xt, xh, ot, oh,
-                          _ptr(positions), _ptr(freqs), dim, int(offset), _choice(layout, ROPE_LAYOUTS, "layout"),
-                          float(amplitude), int(bool(inverse)), _stream()), "svt_rope")
+    pairs = freqs.numel()
+    at, fr = _shaped(positions, "positions", torch.int32, (T,)), _shaped(freqs, "freqs", torch.float64, (pairs,))
+    stream = _launch_on(x, positions=positions, freqs=freqs, out=out)
+    _check(lib().svt_rope(x.data_ptr(), out.data_ptr(), 1 if dtype == torch.float32 else 0, T, H, D, xt, xh, ot, oh, at,
+                          fr, 2 * pairs, offset, _choice(layout, ROPE_LAYOUTS, "layout"), amplitude,
+                          1 if inverse else 0, stream), "svt_rope")
     return out
 
 
@@ -391,48 +402,45 @@ def rope_append(latent, k_rope, positions, slots, kv: KVCache, freqs, *, layout:
     strided) to cache rows slots [T] (negative: skipped); with q_rope [T, H, 64] it rotates the
     queries' rope columns into q_out (a new tensor when None; q[..., 512:] of a [T, H, 576] q fits)
     in the same launch. Returns q_out."""
+    bf16 = torch.bfloat16
     for name, t, width in (("latent", latent, 512), ("k_rope", k_rope, 64)):
-        if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1:
+        if t.dtype != bf16 or t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1:
             raise TypeError(f"{name} must be a bf16 [T, {width}] tensor with unit column stride")
     T = latent.shape[0]
     if k_rope.shape[0] != T:
         raise TypeError("latent and k_rope must have the same number of rows")
-    _shaped(_i32(positions, "positions"), "positions", torch.int32, (T,))
-    _shaped(_i32(slots, "slots"), "slots", torch.int32, (T,))
-    _shaped(_freqs(freqs), "freqs", torch.float64, (32,))
+    at, sl = _shaped(positions, "positions", torch.int32, (T,)), _shaped(slots, "slots", torch.int32, (T,))
+    fr = _shaped(freqs, "freqs", torch.float64, (32,))
+    qi = qo = None
     H = qt = qh = ot = oh = 0
     if q_rope is not None:
         if q_out is None:
-            q_out = torch.empty(q_rope.shape, dtype=q_rope.dtype, device=q_rope.device)
-        for name, t in (("q_rope", q_rope), ("q_out", q_out)):
-            if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != T or t.shape[2] != 64:
-                raise TypeError(f"{name} must be a bf16 [T, H, 64] tensor")
-        if q_out.shape != q_rope.shape:
-            raise TypeError("q_rope and q_out must have the same shape")
+            q_out = torch.empty(q_rope.shape, dtype=bf16, device=q_rope.device)
+        if q_rope.dtype != bf16 or q_rope.dim() != 3 or q_rope.shape[0] != T or q_rope.shape[2] != 64:
+            raise TypeError("q_rope must be a bf16 [T, H, 64] tensor")
+        if q_out.dtype != bf16 or q_out.shape != q_rope.shape:
+            raise TypeError("q_out must have q_rope's type and shape")
         _, H, _, qt, qh = _rows3(q_rope, "q_rope")
         _, _, _, ot, oh = _rows3(q_out, "q_out")
+        if H > 0:
+            qi, qo = q_rope.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise TypeError("q_out needs q_rope")
-    _on_device(latent.device, k_rope=k_rope, positions=positions, slots=slots, kv=kv.data, freqs=freqs, q_rope=q_rope,
-               q_out=q_out)
+    stream = _launch_on(latent, k_rope=k_rope, positions=positions, slots=slots, kv=kv.data, freqs=freqs,
+                        q_rope=q_rope, q_out=q_out)
     _cache_fits(kv)
     ws = default_workspace() if ws is None else ws
-    kvc = kv._c()
-    lat_stride = latent.stride(0) if T > 1 else 512
-    kr_stride = k_rope.stride(0) if T > 1 else 64
-    with_q = q_rope is not None and H > 0
-    _check(lib().svt_rope_append(_ptr(latent), lat_stride, _ptr(k_rope), kr_stride, _ptr(positions), _ptr(slots), T,
-                                 ctypes.byref(kvc), _ptr(freqs), _choice(layout, ROPE_LAYOUTS, "layout"),
-                                 float(amplitude), _ptr(q_rope) if with_q else None, H, qt, qh,
-                                 _ptr(q_out) if with_q else None, ot, oh, ws.ptr, ws.nbytes, _stream()),
-           "svt_rope_append")
+    _check(lib().svt_rope_append(latent.data_ptr(), latent.stride(0) if T > 1 else 512, k_rope.data_ptr(),
+                                 k_rope.stride(0) if T > 1 else 64, at, sl, T, ctypes.byref(kv._c()), fr,
+                                 _choice(layout, ROPE_LAYOUTS, "layout"), amplitude, qi, H, qt, qh, qo, ot, oh,
+                                 ws.buf.data_ptr(), ws.buf.numel(), stream), "svt_rope_append")
     return q_out
 
 
 def _cache_fits(kv: KVCache) -> None:
     """The cache's tensor holds the rows its descriptor promises."""
-    row = kv.row_stride_bytes or ROW_BYTES.get(kv.dtype, 0)
-    if kv.num_slots and kv.data.numel() * kv.data.element_size() < (kv.num_slots - 1) * row + ROW_BYTES.get(kv.dtype, 0):
+    row = ROW_BYTES.get(kv.dtype, 0)
+    if kv.data.nbytes < (kv.num_pages * kv.page_size - 1) * (kv.row_stride_bytes or row) + row:
         raise TypeError("kv data is smaller than num_pages * page_size rows")
 
 
@@ -442,41 +450,35 @@ def sparse_mla_backward(q, kv: KVCache, topk, softmax_scale: float, out, lse, do
     """svt_sparse_mla_backward: the gradients of sparse_mla_decode (or of a grouped prefill, with each
     query's own list). out and lse are the forward's; dout (and dlse) their gradients. Returns
     (dq [T, H, 576] bf16, dkv [num_slots, 576] bf16, weights [T, K] fp32 or None)."""
-    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != 576 or not q.is_contiguous():
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    if q.dtype != bf16 or q.dim() != 3 or q.shape[2] != 576 or not q.is_contiguous():
         raise TypeError("q must be a contiguous bf16 [T, H, 576] tensor")
     T, H, _ = q.shape
-    topk = _i32(topk, "topk")
     if topk.dim() != 2 or topk.shape[0] != T:
         raise TypeError("topk must be an int32 [T, K] tensor")
-    K = topk.shape[1]
-    _shaped(out, "out", torch.bfloat16, (T, H, 512))
-    _shaped(dout, "dout", torch.bfloat16, (T, H, 512))
-    _shaped(lse, "lse", torch.float32, (T, H))
-    _shaped(dlse, "dlse", torch.float32, (T, H))
-    bt = _i32(block_table, "block_table")
-    if bt is not None and bt.dim() != 2:
-        raise TypeError("block_table must be [num_reqs, max_blocks]")
-    if bt is not None and seq_lens is not None:
-        _shaped(_i32(seq_lens, "seq_lens"), "seq_lens", torch.int32, (bt.shape[0],))
-    _shaped(_i32(req_of_token, "req_of_token"), "req_of_token", torch.int32, (T,))
-    _shaped(_i32(topk_len, "topk_len"), "topk_len", torch.int32, (T,))
+    K, n = topk.shape[1], kv.num_slots
+    reqs, blocks = (0, 0) if block_table is None else block_table.shape
     if dq is None:
-        dq = torch.empty((T, H, 576), dtype=torch.bfloat16, device=q.device)
+        dq = torch.empty((T, H, 576), dtype=bf16, device=q.device)
     if dkv is None:
-        dkv = torch.empty((kv.num_slots, 576), dtype=torch.bfloat16, device=q.device)
-    _shaped(dq, "dq", torch.bfloat16, (T, H, 576))
-    _shaped(dkv, "dkv", torch.bfloat16, (kv.num_slots, 576))
-    weights = torch.empty((T, K), dtype=torch.float32, device=q.device) if return_weights else None
-    _on_device(q.device, kv=kv.data, topk=topk, out=out, lse=lse, dout=dout, dlse=dlse, block_table=bt,
-               seq_lens=seq_lens, req_of_token=req_of_token, topk_len=topk_len, dq=dq, dkv=dkv)
+        dkv = torch.empty((n, 576), dtype=bf16, device=q.device)
+    weights = torch.empty((T, K), dtype=f32, device=q.device) if return_weights else None
+    stream = _launch_on(q, kv=kv.data, topk=topk, out=out, lse=lse, dout=dout, dlse=dlse, block_table=block_table,
+                        seq_lens=seq_lens, req_of_token=req_of_token, topk_len=topk_len, dq=dq, dkv=dkv)
     _cache_fits(kv)
-    ws = (ws or default_workspace()).ensure(lib().svt_sparse_mla_backward_workspace_size(T, H, K, kv.num_slots))
-    kvc = kv._c()
-    _check(lib().svt_sparse_mla_backward(_ptr(q), T, H, ctypes.byref(kvc), _ptr(bt), 0 if bt is None else bt.shape[0],
-                                         0 if bt is None else bt.shape[1], _ptr(req_of_token), _ptr(seq_lens),
-                                         _ptr(topk), K, _ptr(topk_len), float(softmax_scale), _ptr(out), _ptr(lse),
-                                         _ptr(dout), _ptr(dlse), _ptr(dq), _ptr(dkv), _ptr(weights), ws.ptr, ws.nbytes,
-                                         _stream()), "svt_sparse_mla_backward")
+    L = lib()
+    ws = (ws or default_workspace()).ensure(L.svt_sparse_mla_backward_workspace_size(T, H, K, n))
+    _check(L.svt_sparse_mla_backward(q.data_ptr(), T, H, ctypes.byref(kv._c()),
+                                     _shaped(block_table, "block_table", i32, (reqs, blocks)), reqs, blocks,
+                                     _shaped(req_of_token, "req_of_token", i32, (T,)),
+                                     _shaped(seq_lens, "seq_lens", i32, (reqs,)) if reqs else None,
+                                     _shaped(topk, "topk", i32, (T, K)), K, _shaped(topk_len, "topk_len", i32, (T,)),
+                                     softmax_scale, _shaped(out, "out", bf16, (T, H, 512)),
+                                     _shaped(lse, "lse", f32, (T, H)), _shaped(dout, "dout", bf16, (T, H, 512)),
+                                     _shaped(dlse, "dlse", f32, (T, H)), _shaped(dq, "dq", bf16, (T, H, 576)),
+                                     _shaped(dkv, "dkv", bf16, (n, 576)),
+                                     None if weights is None else weights.data_ptr(), ws.buf.data_ptr(),
+                                     ws.buf.numel(), stream), "svt_sparse_mla_backward")
     return dq, dkv, weights
 
 
@@ -485,30 +487,29 @@ def distill_topk(scores, topk, teacher, *, lens=None, temperature: float = 1.0, 
     """svt_distill_topk: per query, KL(teacher's top entries || softmax of scores) and the gradient of
     row_weight . loss. scores [T, N] fp32 or bf16 (rows may be strided), topk [T, K] positions (-1 =
     none), teacher [T, K] fp32 weights or logits. Returns (loss [T], dscores [T, N] or None)."""
-    if scores.dtype not in (torch.float32, torch.bfloat16) or scores.dim() != 2 or (
-            scores.shape[1] > 1 and scores.stride(1) != 1):
-        raise TypeError("scores must be an fp32 or bf16 [T, N] tensor with unit column stride")
-    T, N = scores.shape
-    topk = _i32(topk, "topk")
+    dtype, f32, i32 = scores.dtype, torch.float32, torch.int32
+    if (dtype != f32 and dtype != torch.bfloat16) or scores.dim() != 2:
+        raise TypeError("scores must be an fp32 or bf16 [T, N] tensor")
+    T, _, N, stride, _ = _rows3(scores, "scores")
     if topk.dim() != 2 or topk.shape[0] != T:
         raise TypeError("topk must be an int32 [T, K] tensor")
     K = topk.shape[1]
-    _shaped(teacher, "teacher", torch.float32, (T, K))
-    _shaped(_i32(lens, "lens"), "lens", torch.int32, (T,))
-    _shaped(row_weight, "row_weight", torch.float32, (T,))
-    loss = torch.empty((T,), dtype=torch.float32, device=scores.device)
+    loss = torch.empty((T,), dtype=f32, device=scores.device)
+    grad, dstride = None, N
     if dscores is None and need_grad:
-        dscores = torch.empty((T, N), dtype=scores.dtype, device=scores.device)
-    if dscores is not None and (dscores.dtype != scores.dtype or dscores.shape != scores.shape or (
-            N > 1 and dscores.stride(1) != 1)):
-        raise TypeError("dscores must have scores' type and shape, with unit column stride")
-    _on_device(scores.device, topk=topk, teacher=teacher, lens=lens, row_weight=row_weight, dscores=dscores)
-    stride = scores.stride(0) if T > 1 else N  # a single row's stride is meaningless (can be 0)
-    dstride = dscores.stride(0) if dscores is not None and T > 1 else N
-    _check(lib().svt_distill_topk(_ptr(scores), 1 if scores.dtype == torch.float32 else 0, T, N, stride, _ptr(lens),
-                                  _ptr(topk), _ptr(teacher), K, _choice(teacher_kind, TEACHER_KINDS, "teacher_kind"),
-                                  _choice(over, DISTILL_SCOPES, "over"), float(temperature), _ptr(row_weight),
-                                  _ptr(loss), _ptr(dscores), dstride, _stream()), "svt_distill_topk")
+        dscores = torch.empty((T, N), dtype=dtype, device=scores.device)
+    if dscores is not None:
+        if dscores.dtype != dtype or dscores.shape != scores.shape:
+            raise TypeError("dscores must have scores' type and shape")
+        dstride, grad = _rows3(dscores, "dscores")[3], dscores.data_ptr()
+    stream = _launch_on(scores, topk=topk, teacher=teacher, lens=lens, row_weight=row_weight, dscores=dscores)
+    _check(lib().svt_distill_topk(scores.data_ptr(), 1 if dtype == f32 else 0, T, N, stride,
+                                  _shaped(lens, "lens", i32, (T,)), _shaped(topk, "topk", i32, (T, K)),
+                                  _shaped(teacher, "teacher", f32, (T, K)), K,
+                                  _choice(teacher_kind, TEACHER_KINDS, "teacher_kind"),
+                                  _choice(over, DISTILL_SCOPES, "over"), temperature,
+                                  _shaped(row_weight, "row_weight", f32, (T,)), loss.data_ptr(), grad, dstride, stream),
+           "svt_distill_topk")
     return loss, dscores
 
 
