@@ -25,6 +25,7 @@
 #include <math_constants.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "device.cuh"
 #include "internal.h"
@@ -47,8 +48,8 @@ constexpr uint32_t kOffDs = kOffP + kBlk;
 constexpr uint32_t kOffMisc = kOffDs + kBlk;
 struct Misc {
   int slot[4][kEntries];  // the tile's cache rows, a ring: scatter may trail the gather by two tiles
-  float weight[kEntries];
-  uint64_t bars[16];
+  float weight[2][kEntries];
+  uint64_t bars[20];
   uint32_t tmem;
   int abort_flag;
 };
@@ -56,14 +57,14 @@ constexpr uint32_t kSmem = kOffMisc + sizeof(Misc) + 1024;
 static_assert(kSmem <= 232448, "backward shared memory");
 
 // barriers
-enum { kBarKvFull, kBarKvFree, kBarS, kBarP, kBarSeg, kBarDq, kBarDqFree, kBarChunk, kBarChunkFree = kBarChunk + 3,
-       kBarDone = kBarChunkFree + 3, kNumBars };
-static_assert(kNumBars <= 16, "barriers");
+enum { kBarKvFull, kBarKvFree, kBarS, kBarP, kBarPFree, kBarSeg, kBarDq, kBarDqFree, kBarBlock,
+       kBarBufFree = kBarBlock + 5, kBarDone = kBarBufFree + 3, kNumBars };
+static_assert(kNumBars <= 20, "barriers");
 
 // tensor memory columns: dq^T in five blocks of 64 (channels 128 mb .. +127, then the 64 rope
-// ones), S^T and dP^T, and a block for dKV^T; the S^T and dP^T columns serve as two more once
-// the softmax has read them
-constexpr uint32_t kTmDq = 0, kTmS = 320, kTmX = 448;
+// ones), S^T and dP^T, and one block of dKV^T; the S^T and dP^T columns hold the tile's first two
+// blocks of dKV^T once the softmax has read them
+constexpr uint32_t kTmDq = 0, kTmS = 320, kTmX = kTmS + 128;
 
 constexpr int kSoftWarps = 8, kScatWarps = 8, kFillWarps = 3;
 constexpr int kScatWarp0 = kSoftWarps, kFillWarp0 = kScatWarp0 + kScatWarps, kMmaWarp = kFillWarp0 + kFillWarps;
@@ -174,68 +175,88 @@ __device__ __forceinline__ void gather_role(const BackwardParams& p, uint8_t* sm
   }
 }
 
+// The one thread that issues the MMAs. Per tile: dq, the first three blocks of dKV, the next tile's
+// S^T and dP^T, the last two blocks, so that the next tile's softmax runs beside products. A
+// descriptor is a base plus a constant: computed anew for each MMA, the issue took longer than the
+// product (80 cycles each).
 __device__ __forceinline__ void mma_role(const BackwardParams& p, uint8_t* smem, uint32_t tmem, uint32_t bars,
                                          const WaitCtl& wc) {
   const uint32_t base = smem_u32(smem);
-  const uint32_t qb = base + kOffQ, kv = base + kOffKv, pb = base + kOffP, ds = base + kOffDs;
+  const uint64_t q_k = smem_desc_sw128(base + kOffQ, 16, 1024), q_mn = smem_desc_sw128(base + kOffQ, 2 * kBlk, 1024);
+  const uint64_t kv_k = smem_desc_sw128(base + kOffKv, 16, 1024), kv_mn = smem_desc_sw128(base + kOffKv, kBlk, 1024);
+  const uint64_t p_k = smem_desc_sw128(base + kOffP, 16, 1024), ds_k = smem_desc_sw128(base + kOffDs, 16, 1024);
+  const uint64_t ds_mn = smem_desc_sw128(base + kOffDs, kBlk, 1024);
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
-  uint32_t g = 0, segs = 0;
+  uint32_t segs = 0;
+  auto scores = [&](uint32_t g) -> bool {
+    // the S^T and dP^T columns last held the previous tile's first two blocks of dKV
+    if (!mbar_wait(bar(kBarKvFull), g & 1, wc)) return false;
+    if (g > 0 && !(mbar_wait(bar(kBarBufFree), (g - 1) & 1, wc) && mbar_wait(bar(kBarBufFree + 1), (g - 1) & 1, wc)))
+      return false;
+    tc_fence_after();
+#pragma unroll
+    for (int kb = 0; kb < 8; ++kb)
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        umma_f16(tmem + kTmS, kv_k + ((kb * kBlk + ks * 32) >> 4), q_k + ((2 * kb * kBlk + ks * 32) >> 4), kIdescS,
+                 (kb | ks) != 0);
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks)
+      umma_f16(tmem + kTmS, kv_k + ((8 * kBlk + ks * 32) >> 4), q_k + ((16 * kBlk + ks * 32) >> 4), kIdescSRope, 1);
+    umma_commit(bar(kBarS));
+    return true;
+  };
+  // block cb of dKV^T into columns d
+  auto block = [&](auto cbc, uint32_t d) {
+    constexpr int cb = decltype(cbc)::value;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks)
+      umma_f16(d, q_mn + ((4 * cb * kBlk + ks * 2048) >> 4), ds_k + ((ks * 32) >> 4), cb < 4 ? kIdescKv : kIdescKvRope,
+               ks > 0);
+    if constexpr (cb < 4) {
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        umma_f16(d, q_mn + (((4 * cb + 1) * kBlk + ks * 2048) >> 4), p_k + ((ks * 32) >> 4), kIdescKv, 1);
+    }
+    umma_commit(bar(kBarBlock + cb));
+  };
+  using std::integral_constant;
+  uint32_t g = 0;
   bool ok = true;
   SegIter it(p);
   Seg s;
   while (ok && it.next(s)) {
     if (s.j0 >= s.j1) continue;
+    ok = scores(g);
     for (int j = s.j0; ok && j < s.j1; ++j, ++g) {
-      ok = mbar_wait(bar(kBarKvFull), g & 1, wc);
-      // the S^T and dP^T columns last held the previous tile's fourth and fifth blocks
-      if (ok && g > 0) ok = mbar_wait(bar(kBarChunkFree), 1, wc) && mbar_wait(bar(kBarChunkFree + 1), 1, wc);
-      if (!ok) break;
-      tc_fence_after();
-#pragma unroll 1
-      for (int kb = 0; kb < 8; ++kb) {
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          umma_f16(tmem + kTmS, smem_desc_sw128(kv + kb * kBlk + ks * 32, 16, 1024),
-                   smem_desc_sw128(qb + 2 * kb * kBlk + ks * 32, 16, 1024), kIdescS, (kb | ks) != 0);
-      }
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-        umma_f16(tmem + kTmS, smem_desc_sw128(kv + 8 * kBlk + ks * 32, 16, 1024),
-                 smem_desc_sw128(qb + 16 * kBlk + ks * 32, 16, 1024), kIdescSRope, 1);
-      umma_commit(bar(kBarS));
       ok = mbar_wait(bar(kBarP), g & 1, wc);
       if (ok && j == s.j0 && segs > 0) ok = mbar_wait(bar(kBarDqFree), (segs - 1) & 1, wc);
       if (!ok) break;
       tc_fence_after();
-#pragma unroll 1
-      for (int mb = 0; mb < 5; ++mb) {
+#pragma unroll
+      for (int mb = 0; mb < 5; ++mb)
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          umma_f16(tmem + kTmDq + 64 * mb, smem_desc_sw128(kv + 2 * mb * kBlk + ks * 2048, kBlk, 1024),
-                   smem_desc_sw128(ds + ks * 2048, kBlk, 1024), mb < 4 ? kIdescDq : kIdescDqRope, j > s.j0 || ks > 0);
-      }
+          umma_f16(tmem + kTmDq + 64 * mb, kv_mn + ((2 * mb * kBlk + ks * 2048) >> 4), ds_mn + ((ks * 2048) >> 4),
+                   mb < 4 ? kIdescDq : kIdescDqRope, j > s.j0 || ks > 0);
       umma_commit(bar(kBarKvFree));
-#pragma unroll 1
-      for (int cb = 0; cb < 5; ++cb) {
-        // blocks go to the S^T, dP^T, third, S^T, dP^T columns; use n of a block waits for use n - 1
-        const int b = cb < 3 ? cb : cb - 3;
-        const uint32_t n = b == 2 ? g : 2 * g + (cb >= 3 ? 1 : 0);
-        if (cb >= 2 && n > 0) ok = mbar_wait(bar(kBarChunkFree + b), (n - 1) & 1, wc);
-        if (!ok) break;
+      block(integral_constant<int, 0>{}, tmem + kTmS);
+      block(integral_constant<int, 1>{}, tmem + kTmS + 64);
+      // the third columns serve three blocks a tile: use n waits until use n - 1 has been read
+      auto third = [&](uint32_t k) {
+        const uint32_t n = 3 * g + k;
+        if (n > 0) ok = ok && mbar_wait(bar(kBarBufFree + 2), (n - 1) & 1, wc);
         tc_fence_after();
-        const uint32_t d = tmem + (b == 2 ? kTmX : kTmS + 64 * b);
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          umma_f16(d, smem_desc_sw128(qb + 4 * cb * kBlk + ks * 2048, 2 * kBlk, 1024),
-                   smem_desc_sw128(ds + ks * 32, 16, 1024), cb < 4 ? kIdescKv : kIdescKvRope, ks > 0);
-        if (cb < 4) {
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma_f16(d, smem_desc_sw128(qb + (4 * cb + 1) * kBlk + ks * 2048, 2 * kBlk, 1024),
-                     smem_desc_sw128(pb + ks * 32, 16, 1024), kIdescKv, 1);
-        }
-        umma_commit(bar(kBarChunk + b));
-      }
+        return ok;
+      };
+      if (!third(0)) break;
+      block(integral_constant<int, 2>{}, tmem + kTmX);
+      if (j + 1 < s.j1 && !(ok = scores(g + 1))) break;
+      if (!third(1)) break;
+      block(integral_constant<int, 3>{}, tmem + kTmX);
+      if (!third(2)) break;
+      block(integral_constant<int, 4>{}, tmem + kTmX);
+      umma_commit(bar(kBarPFree));
     }
     umma_commit(bar(kBarSeg));
     umma_commit(bar(kBarDq));
@@ -268,14 +289,30 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
       lse2[i] = v.x;
       delta[i] = v.y;
     }
+    // an entry's weight: the two warps of a quadrant hold half of the heads each; the second leaves its
+    // half in shared memory, the first adds them a tile later, when the barriers between have made
+    // them visible
+    float held = 0.f;
+    bool held_live = false;
+    auto put_weight = [&](int j) {
+      const int k = j * kEntries + e;
+      if (half == 0 && !odd && held_live && k < p.K) {
+        float* dst = p.weights + static_cast<long long>(s.t) * p.K + k;
+        const float w = held + misc->weight[(g - 1) & 1][e];
+        // two head chunks add to a zero: the same sum in either order
+        if (p.hchunks > 1) atomicAdd(dst, w);
+        else *dst = w;
+      }
+    };
     for (int j = s.j0; j < s.j1; ++j, ++g) {
       mbar_wait(bar(kBarS), g & 1, wc);
       tc_fence_after();
       uint32_t sv[16], dv[16];
       tmem_ld_16x64b_x16(lanes + kTmS + 32 * half, sv);
       tmem_ld_16x64b_x16(lanes + kTmS + 64 + 32 * half, dv);
-      tmem_ld_wait();
       const bool live = misc->slot[g & 3][e] >= 0;
+      if (p.weights != nullptr && j > s.j0) put_weight(j - 1);
+      tmem_ld_wait();
       float w = 0.f;
       uint32_t pk[16];
 #pragma unroll
@@ -286,31 +323,39 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
         w += pr;
         pk[i] = pack_bf16x2(pr, d);
       }
+      if (p.weights != nullptr) {
+        w += __shfl_xor_sync(0xffffffffu, w, 2);
+        if (half == 1 && !odd) misc->weight[g & 1][e] = w;
+        held = w;
+        held_live = live;
+      }
       // neighbours hold the even and the odd heads of an entry: one shuffle each, and the even one
-      // writes the row of P, the odd one the row of dS
+      // writes the row of P, the odd one the row of dS. The four lanes that write to the same chunk's
+      // banks take the row's four chunks in different orders (two wavefronts an 8-lane phase instead
+      // of four)
       uint32_t out[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const uint32_t o = __shfl_xor_sync(0xffffffffu, pk[i], 2);
         out[i] = odd ? __byte_perm(o, pk[i], 0x7632) : __byte_perm(pk[i], o, 0x5410);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool s1 = (lane & 1) != 0, s2 = odd != 0;
+        const uint32_t a0 = s1 ? out[4 + i] : out[i], a1 = s1 ? out[i] : out[4 + i];
+        const uint32_t a2 = s1 ? out[12 + i] : out[8 + i], a3 = s1 ? out[8 + i] : out[12 + i];
+        out[i] = s2 ? a2 : a0;
+        out[4 + i] = s2 ? a3 : a1;
+        out[8 + i] = s2 ? a0 : a2;
+        out[12 + i] = s2 ? a1 : a3;
+      }
+      // the last tile's products with P and dS are done
+      if (g > 0) mbar_wait(bar(kBarPFree), (g - 1) & 1, wc);
       uint8_t* dst = smem + (odd ? kOffDs : kOffP);
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        *reinterpret_cast<uint4*>(dst + sw128_offset(e, 4 * half + v)) =
+        *reinterpret_cast<uint4*>(dst + sw128_offset(e, 4 * half + (v ^ (lane & 3)))) =
             make_uint4(out[4 * v], out[4 * v + 1], out[4 * v + 2], out[4 * v + 3]);
-      if (p.weights != nullptr) {
-        w += __shfl_xor_sync(0xffffffffu, w, 2);
-        if (half == 1 && !odd) misc->weight[e] = w;
-        named_bar_sync(1 + quad, 64);
-        const int k = j * kEntries + e;
-        if (half == 0 && !odd && live && k < p.K) {
-          float* dstw = p.weights + static_cast<long long>(s.t) * p.K + k;
-          // two head chunks add to a zero: the same sum in either order
-          if (p.hchunks > 1) atomicAdd(dstw, w + misc->weight[e]);
-          else *dstw = w + misc->weight[e];
-        }
-      }
       fence_proxy_async_smem();  // P and dS -> MMA operand reads
       tc_fence_before();
       mbar_arrive(bar(kBarP));
@@ -319,6 +364,7 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
     if (any) {
       mbar_wait(bar(kBarDq), segs & 1, wc);
       tc_fence_after();
+      if (p.weights != nullptr) put_weight(s.j1 - 1);
     }
 #pragma unroll 1
     for (int mb = 0; mb < 5; ++mb) {
@@ -367,16 +413,17 @@ __device__ __forceinline__ void scatter_role(const BackwardParams& p, Misc* misc
 #pragma unroll 1
       for (int cb = 0; cb < 5; ++cb) {
         if (((5 * g + cb) & 1) != group) continue;
-        const int b = cb < 3 ? cb : cb - 3;
-        const uint32_t n = b == 2 ? g : 2 * g + (cb >= 3 ? 1 : 0);
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarChunk + b), n & 1, wc))) return;
+        // a group meets every second phase of a block's barrier; it has waited for a later block of
+        // the tile between, so the phase it skipped is complete
+        const int b = cb < 2 ? cb : 2;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarBlock + cb), g & 1, wc))) return;
         tc_fence_after();
         uint32_t v[2][32];
-        tmem_ld32(lanes + (b == 2 ? kTmX : kTmS + 64 * b), v[0]);
-        tmem_ld32(lanes + (b == 2 ? kTmX : kTmS + 64 * b) + 32, v[1]);
+        tmem_ld32(lanes + kTmS + 64 * b, v[0]);
+        tmem_ld32(lanes + kTmS + 64 * b + 32, v[1]);
         tmem_ld_wait();
         tc_fence_before();
-        mbar_arrive(bar(kBarChunkFree + b));
+        mbar_arrive(bar(kBarBufFree + b));
         if (cb == 4 && lane >= 16) continue;
         float* dst = p.dkv_acc + 128 * cb + (cb < 4 ? 32 : 16) * quad + lane;
         const int4* slots = reinterpret_cast<const int4*>(misc->slot[g & 3]);
@@ -404,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const BackwardPar
       int count = 1;
       if (i == kBarKvFull) count = kFillThreads;
       if (i == kBarP || i == kBarDqFree) count = 32 * kSoftWarps;
-      if (i >= kBarChunkFree && i < kBarChunkFree + 3) count = 128;
+      if (i >= kBarBufFree && i < kBarBufFree + 3) count = 128;
       mbar_init(bars + 8 * i, count);
     }
     misc->abort_flag = 0;
