@@ -266,6 +266,18 @@ __device__ __forceinline__ void mma_role(const BackwardParams& p, uint8_t* smem,
   mbar_wait_ignoring_abort(bar(kBarDone), 0, wc);  // nothing runs when tensor memory is released
 }
 
+// Adds v[e] to dst of cache row slots[e], e < 32 (the warp's lanes are consecutive channels).
+__device__ __forceinline__ void add_rows(float* dst, const int* slots, const uint32_t (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int4 s = reinterpret_cast<const int4*>(slots)[i];
+    if (s.x >= 0) atomicAdd(dst + static_cast<long long>(s.x) * kRow, __uint_as_float(v[4 * i]));
+    if (s.y >= 0) atomicAdd(dst + static_cast<long long>(s.y) * kRow, __uint_as_float(v[4 * i + 1]));
+    if (s.z >= 0) atomicAdd(dst + static_cast<long long>(s.z) * kRow, __uint_as_float(v[4 * i + 2]));
+    if (s.w >= 0) atomicAdd(dst + static_cast<long long>(s.w) * kRow, __uint_as_float(v[4 * i + 3]));
+  }
+}
+
 __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* smem, Misc* misc, uint32_t tmem,
                                              uint32_t bars, const WaitCtl& wc) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -359,6 +371,16 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
       fence_proxy_async_smem();  // P and dS -> MMA operand reads
       tc_fence_before();
       mbar_arrive(bar(kBarP));
+      // these warps wait for the next scores now: meanwhile they add the first block of dKV^T, half of
+      // the entries each
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarBlock), g & 1, wc))) continue;
+      tc_fence_after();
+      uint32_t v[32];
+      tmem_ld32(lanes + kTmS + 32 * half, v);
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(bar(kBarBufFree));
+      add_rows(p.dkv_acc + 32 * quad + lane, misc->slot[g & 3] + 32 * half, v);
     }
     // dq^T: lane = channel, this warp's heads 32 half .. + 31
     if (any) {
@@ -402,7 +424,7 @@ __device__ __forceinline__ void scatter_role(const BackwardParams& p, Misc* misc
                                              const WaitCtl& wc) {
   const int warp = (threadIdx.x >> 5) - kScatWarp0, lane = threadIdx.x & 31;
   const int quad = warp & 3;
-  const uint32_t group = static_cast<uint32_t>(warp >> 2);  // takes every second block
+  const int group = warp >> 2;  // takes blocks 1 and 3, or 2 and 4
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
   const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
   uint32_t g = 0;
@@ -411,10 +433,7 @@ __device__ __forceinline__ void scatter_role(const BackwardParams& p, Misc* misc
   while (it.next(s)) {
     for (int j = s.j0; j < s.j1; ++j, ++g) {
 #pragma unroll 1
-      for (int cb = 0; cb < 5; ++cb) {
-        if (((5 * g + cb) & 1) != group) continue;
-        // a group meets every second phase of a block's barrier; it has waited for a later block of
-        // the tile between, so the phase it skipped is complete
+      for (int cb = 1 + group; cb < 5; cb += 2) {
         const int b = cb < 2 ? cb : 2;
         if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarBlock + cb), g & 1, wc))) return;
         tc_fence_after();
@@ -426,15 +445,8 @@ __device__ __forceinline__ void scatter_role(const BackwardParams& p, Misc* misc
         mbar_arrive(bar(kBarBufFree + b));
         if (cb == 4 && lane >= 16) continue;
         float* dst = p.dkv_acc + 128 * cb + (cb < 4 ? 32 : 16) * quad + lane;
-        const int4* slots = reinterpret_cast<const int4*>(misc->slot[g & 3]);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int4 sl = slots[i];
-          const int a[4] = {sl.x, sl.y, sl.z, sl.w};
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (a[u] >= 0) atomicAdd(dst + static_cast<long long>(a[u]) * kRow, __uint_as_float(v[i >> 3][(4 * i + u) & 31]));
-        }
+        add_rows(dst, misc->slot[g & 3], v[0]);
+        add_rows(dst, misc->slot[g & 3] + 32, v[1]);
       }
     }
   }
@@ -451,7 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const BackwardPar
       int count = 1;
       if (i == kBarKvFull) count = kFillThreads;
       if (i == kBarP || i == kBarDqFree) count = 32 * kSoftWarps;
-      if (i >= kBarBufFree && i < kBarBufFree + 3) count = 128;
+      if (i == kBarBufFree) count = 32 * kSoftWarps;
+      if (i == kBarBufFree + 1 || i == kBarBufFree + 2) count = 128;
       mbar_init(bars + 8 * i, count);
     }
     misc->abort_flag = 0;
