@@ -58,13 +58,13 @@ static_assert(kSmem <= 232448, "backward shared memory");
 
 // barriers
 enum { kBarKvFull, kBarKvFree, kBarS, kBarP, kBarPFree, kBarSeg, kBarDq, kBarDqFree, kBarBlock,
-       kBarBufFree = kBarBlock + 5, kBarDone = kBarBufFree + 3, kNumBars };
+       kBarBlockFree = kBarBlock + 5, kBarDone = kBarBlockFree + 5, kNumBars };
 static_assert(kNumBars <= 20, "barriers");
 
 // tensor memory columns: dq^T in five blocks of 64 (channels 128 mb .. +127, then the 64 rope
-// ones), S^T and dP^T, and one block of dKV^T; the S^T and dP^T columns hold the tile's first two
-// blocks of dKV^T once the softmax has read them
-constexpr uint32_t kTmDq = 0, kTmS = 320, kTmX = kTmS + 128;
+// ones), S^T, dP^T, and a block of dKV^T. The S^T columns hold blocks 0 and 3 of dKV^T and the dP^T
+// columns block 1 once the softmax has read them; the others go to the last columns
+constexpr uint32_t kTmDq = 0, kTmS = 320, kTmDp = kTmS + 64, kTmX = kTmDp + 64;
 
 constexpr int kSoftWarps = 8, kScatWarps = 8, kFillWarps = 3;
 constexpr int kScatWarp0 = kSoftWarps, kFillWarp0 = kScatWarp0 + kScatWarps, kMmaWarp = kFillWarp0 + kFillWarps;
@@ -175,9 +175,8 @@ __device__ __forceinline__ void gather_role(const BackwardParams& p, uint8_t* sm
   }
 }
 
-// The one thread that issues the MMAs. Per tile: dq, the first three blocks of dKV, the next tile's
-// S^T and dP^T, the last two blocks, so that the next tile's softmax runs beside products. A
-// descriptor is a base plus a constant: computed anew for each MMA, the issue took longer than the
+// The one thread that issues the MMAs. Per tile: dq (which frees the rows' tile), four blocks of dKV
+// while the next rows land, the next tile's S^T and dP^T, the last block. A descriptor is a base plus a constant: computed anew for each MMA, the issue took longer than the
 // product (80 cycles each).
 __device__ __forceinline__ void mma_role(const BackwardParams& p, uint8_t* smem, uint32_t tmem, uint32_t bars,
                                          const WaitCtl& wc) {
@@ -189,9 +188,9 @@ __device__ __forceinline__ void mma_role(const BackwardParams& p, uint8_t* smem,
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
   uint32_t segs = 0;
   auto scores = [&](uint32_t g) -> bool {
-    // the S^T and dP^T columns last held the previous tile's first two blocks of dKV
+    // the S^T and dP^T columns last held the previous tile's blocks 3 and 1
     if (!mbar_wait(bar(kBarKvFull), g & 1, wc)) return false;
-    if (g > 0 && !(mbar_wait(bar(kBarBufFree), (g - 1) & 1, wc) && mbar_wait(bar(kBarBufFree + 1), (g - 1) & 1, wc)))
+    if (g > 0 && !(mbar_wait(bar(kBarBlockFree + 1), (g - 1) & 1, wc) && mbar_wait(bar(kBarBlockFree + 3), (g - 1) & 1, wc)))
       return false;
     tc_fence_after();
 #pragma unroll
@@ -241,20 +240,16 @@ __device__ __forceinline__ void mma_role(const BackwardParams& p, uint8_t* smem,
                    mb < 4 ? kIdescDq : kIdescDqRope, j > s.j0 || ks > 0);
       umma_commit(bar(kBarKvFree));
       block(integral_constant<int, 0>{}, tmem + kTmS);
-      block(integral_constant<int, 1>{}, tmem + kTmS + 64);
-      // the third columns serve three blocks a tile: use n waits until use n - 1 has been read
-      auto third = [&](uint32_t k) {
-        const uint32_t n = 3 * g + k;
-        if (n > 0) ok = ok && mbar_wait(bar(kBarBufFree + 2), (n - 1) & 1, wc);
-        tc_fence_after();
-        return ok;
-      };
-      if (!third(0)) break;
+      block(integral_constant<int, 1>{}, tmem + kTmDp);
+      if (g > 0 && !(ok = mbar_wait(bar(kBarBlockFree + 4), (g - 1) & 1, wc))) break;
+      tc_fence_after();
       block(integral_constant<int, 2>{}, tmem + kTmX);
+      if (!(ok = mbar_wait(bar(kBarBlockFree), g & 1, wc))) break;
+      tc_fence_after();
+      block(integral_constant<int, 3>{}, tmem + kTmS);
       if (j + 1 < s.j1 && !(ok = scores(g + 1))) break;
-      if (!third(1)) break;
-      block(integral_constant<int, 3>{}, tmem + kTmX);
-      if (!third(2)) break;
+      if (!(ok = mbar_wait(bar(kBarBlockFree + 2), g & 1, wc))) break;
+      tc_fence_after();
       block(integral_constant<int, 4>{}, tmem + kTmX);
       umma_commit(bar(kBarPFree));
     }
@@ -283,34 +278,39 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3, half = warp >> 2;
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
-  // S^T (64 entries in lanes 0-15 of each quadrant): this thread's entry, and its heads 32 half +
-  // 2 i + odd
-  const int e = 16 * quad + (lane >> 2) + 8 * (lane & 1), odd = (lane >> 1) & 1;
+  // S^T and dP^T (64 entries in lanes 0-15 of each quadrant): this thread's entries e and e + 8, and
+  // their heads 32 half + 8 k + 2 (lane & 3) and the next, k < 4
+  const int e = 16 * quad + (lane >> 2), pair = lane & 3;
   const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
   const float scale_log2 = p.scale * kLog2e;
+  // where this lane's row of the stored 8 x 8 matrices goes: matrix lane >> 3 is chunk 4 half + that
+  const uint32_t at0 = smem_u32(smem) + sw128_offset(16 * quad + (lane & 7), 4 * half + (lane >> 3));
+  const uint32_t at8 = at0 + 8 * 128;
+  // an entry's weight: the two warps of a quadrant hold half of the heads each. Lanes 0 and 1 of four
+  // keep the sums of e and e + 8
+  const int we = e + 8 * (pair & 1);
   uint32_t g = 0, segs = 0;
   SegIter it(p);
   Seg s;
   while (it.next(s)) {
     const bool any = s.j0 < s.j1;
-    float lse2[16], delta[16];
+    float lse2[8], delta[8];  // delta times the softmax scale
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = 32 * half + 2 * i + odd;
+    for (int i = 0; i < 8; ++i) {
+      const int r = 32 * half + 8 * (i >> 1) + 2 * pair + (i & 1);
       const float2 v = r < s.nvalid ? p.stats[s.base + r] : make_float2(CUDART_INF_F, 0.f);
       lse2[i] = v.x;
-      delta[i] = v.y;
+      delta[i] = v.y * p.scale;
     }
-    // an entry's weight: the two warps of a quadrant hold half of the heads each; the second leaves its
-    // half in shared memory, the first adds them a tile later, when the barriers between have made
-    // them visible
+    // the second half leaves its sums in shared memory, the first adds them a tile later, when the
+    // barriers between have made them visible
     float held = 0.f;
     bool held_live = false;
     auto put_weight = [&](int j) {
-      const int k = j * kEntries + e;
-      if (half == 0 && !odd && held_live && k < p.K) {
+      const int k = j * kEntries + we;
+      if (half == 0 && pair < 2 && held_live && k < p.K) {
         float* dst = p.weights + static_cast<long long>(s.t) * p.K + k;
-        const float w = held + misc->weight[(g - 1) & 1][e];
+        const float w = held + misc->weight[(g - 1) & 1][we];
         // two head chunks add to a zero: the same sum in either order
         if (p.hchunks > 1) atomicAdd(dst, w);
         else *dst = w;
@@ -320,67 +320,63 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
       mbar_wait(bar(kBarS), g & 1, wc);
       tc_fence_after();
       uint32_t sv[16], dv[16];
-      tmem_ld_16x64b_x16(lanes + kTmS + 32 * half, sv);
-      tmem_ld_16x64b_x16(lanes + kTmS + 64 + 32 * half, dv);
-      const bool live = misc->slot[g & 3][e] >= 0;
+      tmem_ld_16x256b_x4(lanes + kTmS + 32 * half, sv);
+      tmem_ld_16x256b_x4(lanes + kTmDp + 32 * half, dv);
+      const bool live0 = misc->slot[g & 3][e] >= 0, live8 = misc->slot[g & 3][e + 8] >= 0;
       if (p.weights != nullptr && j > s.j0) put_weight(j - 1);
       tmem_ld_wait();
-      float w = 0.f;
-      uint32_t pk[16];
+      uint32_t pp[8], pd[8];  // [2 k]: entry e, [2 k + 1]: entry e + 8
+      float w0 = 0.f, w8 = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float x = ex2_approx(fmaf(__uint_as_float(sv[i]), scale_log2, -lse2[i]));
-        const float pr = live ? x : 0.f;
-        const float d = live ? pr * (__uint_as_float(dv[i]) - delta[i]) * p.scale : 0.f;
-        w += pr;
-        pk[i] = pack_bf16x2(pr, d);
-      }
-      if (p.weights != nullptr) {
-        w += __shfl_xor_sync(0xffffffffu, w, 2);
-        if (half == 1 && !odd) misc->weight[g & 1][e] = w;
-        held = w;
-        held_live = live;
-      }
-      // neighbours hold the even and the odd heads of an entry: one shuffle each, and the even one
-      // writes the row of P, the odd one the row of dS. The four lanes that write to the same chunk's
-      // banks take the row's four chunks in different orders (two wavefronts an 8-lane phase instead
-      // of four)
-      uint32_t out[16];
+      for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t o = __shfl_xor_sync(0xffffffffu, pk[i], 2);
-        out[i] = odd ? __byte_perm(o, pk[i], 0x7632) : __byte_perm(pk[i], o, 0x5410);
-      }
+        for (int h = 0; h < 2; ++h) {
+          float pr[2], d[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool s1 = (lane & 1) != 0, s2 = odd != 0;
-        const uint32_t a0 = s1 ? out[4 + i] : out[i], a1 = s1 ? out[i] : out[4 + i];
-        const uint32_t a2 = s1 ? out[12 + i] : out[8 + i], a3 = s1 ? out[8 + i] : out[12 + i];
-        out[i] = s2 ? a2 : a0;
-        out[4 + i] = s2 ? a3 : a1;
-        out[8 + i] = s2 ? a0 : a2;
-        out[12 + i] = s2 ? a1 : a3;
-      }
+          for (int u = 0; u < 2; ++u) {
+            const int i = 4 * k + 2 * h + u;
+            // a dead entry's row is zero: with P = 0, its dS is 0 too
+            const float x = ex2_approx(fmaf(__uint_as_float(sv[i]), scale_log2, -lse2[2 * k + u]));
+            pr[u] = (h ? live8 : live0) ? x : 0.f;
+            d[u] = pr[u] * fmaf(__uint_as_float(dv[i]), p.scale, -delta[2 * k + u]);
+            if (h) w8 += pr[u];
+            else w0 += pr[u];
+          }
+          pp[2 * k + h] = pack_bf16x2(pr[0], pr[1]);
+          pd[2 * k + h] = pack_bf16x2(d[0], d[1]);
+        }
       // the last tile's products with P and dS are done
       if (g > 0) mbar_wait(bar(kBarPFree), (g - 1) & 1, wc);
-      uint8_t* dst = smem + (odd ? kOffDs : kOffP);
+      stmatrix_x4(at0 + kOffP, pp[0], pp[2], pp[4], pp[6]);
+      stmatrix_x4(at8 + kOffP, pp[1], pp[3], pp[5], pp[7]);
+      stmatrix_x4(at0 + kOffDs, pd[0], pd[2], pd[4], pd[6]);
+      stmatrix_x4(at8 + kOffDs, pd[1], pd[3], pd[5], pd[7]);
+      if (p.weights != nullptr) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        *reinterpret_cast<uint4*>(dst + sw128_offset(e, 4 * half + (v ^ (lane & 3)))) =
-            make_uint4(out[4 * v], out[4 * v + 1], out[4 * v + 2], out[4 * v + 3]);
+        for (int o = 1; o < 4; o <<= 1) {
+          w0 += __shfl_xor_sync(0xffffffffu, w0, o);
+          w8 += __shfl_xor_sync(0xffffffffu, w8, o);
+        }
+        held = pair ? w8 : w0;
+        held_live = pair ? live8 : live0;
+        if (half == 1 && pair < 2) misc->weight[g & 1][we] = held;
+      }
       fence_proxy_async_smem();  // P and dS -> MMA operand reads
       tc_fence_before();
       mbar_arrive(bar(kBarP));
-      // these warps wait for the next scores now: meanwhile they add the first block of dKV^T, half of
-      // the entries each
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarBlock), g & 1, wc))) continue;
-      tc_fence_after();
-      uint32_t v[32];
-      tmem_ld32(lanes + kTmS + 32 * half, v);
-      tmem_ld_wait();
-      tc_fence_before();
-      mbar_arrive(bar(kBarBufFree));
-      add_rows(p.dkv_acc + 32 * quad + lane, misc->slot[g & 3] + 32 * half, v);
+      // these warps wait for the next scores now: meanwhile they add blocks 0 and 3 of dKV^T, half of the
+      // entries each
+#pragma unroll 1
+      for (int cb = 0; cb < 4; cb += 3) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarBlock + cb), g & 1, wc))) break;
+        tc_fence_after();
+        uint32_t v[32];
+        tmem_ld32(lanes + kTmS + 32 * half, v);
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(bar(kBarBlockFree + cb));
+        add_rows(p.dkv_acc + 128 * cb + 32 * quad + lane, misc->slot[g & 3] + 32 * half, v);
+      }
     }
     // dq^T: lane = channel, this warp's heads 32 half .. + 31
     if (any) {
@@ -424,7 +420,7 @@ __device__ __forceinline__ void scatter_role(const BackwardParams& p, Misc* misc
                                              const WaitCtl& wc) {
   const int warp = (threadIdx.x >> 5) - kScatWarp0, lane = threadIdx.x & 31;
   const int quad = warp & 3;
-  const int group = warp >> 2;  // takes blocks 1 and 3, or 2 and 4
+  const int group = warp >> 2;  // takes blocks 1 and 4, or 2
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
   const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
   uint32_t g = 0;
@@ -433,16 +429,16 @@ __device__ __forceinline__ void scatter_role(const BackwardParams& p, Misc* misc
   while (it.next(s)) {
     for (int j = s.j0; j < s.j1; ++j, ++g) {
 #pragma unroll 1
-      for (int cb = 1 + group; cb < 5; cb += 2) {
-        const int b = cb < 2 ? cb : 2;
+      for (int cb = 1 + group; cb < 5; cb += 3) {
+        const uint32_t from = cb == 1 ? kTmDp : kTmX;
         if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarBlock + cb), g & 1, wc))) return;
         tc_fence_after();
         uint32_t v[2][32];
-        tmem_ld32(lanes + kTmS + 64 * b, v[0]);
-        tmem_ld32(lanes + kTmS + 64 * b + 32, v[1]);
+        tmem_ld32(lanes + from, v[0]);
+        tmem_ld32(lanes + from + 32, v[1]);
         tmem_ld_wait();
         tc_fence_before();
-        mbar_arrive(bar(kBarBufFree + b));
+        mbar_arrive(bar(kBarBlockFree + cb));
         if (cb == 4 && lane >= 16) continue;
         float* dst = p.dkv_acc + 128 * cb + (cb < 4 ? 32 : 16) * quad + lane;
         add_rows(dst, misc->slot[g & 3], v[0]);
@@ -463,8 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const BackwardPar
       int count = 1;
       if (i == kBarKvFull) count = kFillThreads;
       if (i == kBarP || i == kBarDqFree) count = 32 * kSoftWarps;
-      if (i == kBarBufFree) count = 32 * kSoftWarps;
-      if (i == kBarBufFree + 1 || i == kBarBufFree + 2) count = 128;
+      if (i >= kBarBlockFree && i < kBarBlockFree + 5) count = 128;
+      if (i == kBarBlockFree || i == kBarBlockFree + 3) count = 32 * kSoftWarps;
       mbar_init(bars + 8 * i, count);
     }
     misc->abort_flag = 0;
