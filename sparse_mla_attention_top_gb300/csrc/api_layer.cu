@@ -258,8 +258,8 @@ svt_status svt_sparse_mla_backward(const void* q_bf16, int32_t T, int32_t H, con
   if (block_table != nullptr && (num_reqs <= 0 || max_blocks <= 0))
     return set_last_error(SVT_ERR_INVALID_ARG, "num_reqs and max_blocks must be > 0 with a block table");
   const long long num_slots = kv->num_pages * static_cast<long long>(kv->page_size);
-  if (static_cast<long long>(T) * H >= (1ll << 31) || static_cast<long long>(T) * K >= (1ll << 40))
-    return set_last_error(SVT_ERR_UNSUPPORTED, "T * H must be below 2^31 and T * K below 2^40");
+  if (static_cast<long long>(T) * H >= (1ll << 30) || static_cast<long long>(T) * K >= (1ll << 40))
+    return set_last_error(SVT_ERR_UNSUPPORTED, "T * H must be below 2^30 and T * K below 2^40");
   svt::BackwardParams p{};
   p.T = T;
   p.H = H;

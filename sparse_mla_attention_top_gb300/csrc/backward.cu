@@ -5,10 +5,10 @@
 // and a cache row's gradient is the sum of dK (+ dV on the latent columns) over the lists that
 // hold it. sum over heads of P is each entry's attention weight.
 //
-// Three kernels. prepare resolves the lists and forms delta and lse in log2 units. The main
-// kernel walks (row-set, 64-entry tile) pairs, a row-set being up to 64 heads of one query, one
-// persistent CTA per SM with an equal share of all tiles (stream-K). finish joins the dq of
-// row-sets cut between CTAs (fp32, in a fixed order) and rounds the cache rows' sums to bf16.
+// Three kernels. prepare resolves the lists, forms delta and lse in log2 units and zeroes the cache
+// rows' sums. The main kernel walks (row-set, 64-entry tile) pairs, a row-set being up to 64 heads of
+// one query, one persistent CTA per SM with an equal share of all tiles (stream-K). finish joins the
+// dq of row-sets cut between CTAs (fp32, in a fixed order) and rounds the cache rows' sums to bf16.
 //
 // Main kernel, per tile, on tcgen05 with fp32 accumulators in tensor memory (e = entry, r = head
 // row, c = channel; the contractions' operands are the tiles as they lie, read K- or MN-major):
@@ -17,11 +17,17 @@
 //   2. dq^T[c, r]         += K^T dS             stays in tensor memory over the row-set's tiles
 //   3. dKV^T[c, e]         = q^T dS + dout^T P  128 channels at a time; each block leaves for
 //                                               fp32 atomic additions as it is done
-// Lane = channel in 3, so a warp adds 128 contiguous bytes of one cache row per instruction.
+// P and dS are the only values rounded before the end (to bf16, as operands).
 //
-// Warps: 8 softmax (S^T, dP^T -> P, dS in bf16; dq out), 8 scatter (dKV^T -> additions), 3 gather
-// (cp.async, rows zero-filled where there is none), 1 that issues the MMAs. q and dout (136 KB)
-// and one 72 KB tile of rows fill shared memory, so the next tile is gathered while step 3 runs.
+// Warps: 8 softmax (S^T, dP^T -> P, dS; two of the five dKV^T blocks -> additions; dq out), 8 scatter
+// (the other blocks -> additions), 3 gather (cp.async, rows zero-filled where there is none), 1 that
+// issues the MMAs. q and dout (136 KB) and one 72 KB tile of rows fill shared memory, so the next
+// tile is gathered while step 3 runs.
+//
+// What bounds it: a tile takes about 4.9 us (9300 cycles). The chain product 1 (2200 cycles) -> softmax
+// (1500) -> product 2 (900) -> product 3 (2300) is 7800 with the additions left out, and the additions
+// alone, 147 KB a tile, 7200 at the 6 TB/s that the L2 takes; they meet in the few buffers between.
+// 1024 queries x 64 heads x 2048 entries: 1.09 ms, 680 TFLOP/s, 4.8 GB of additions.
 #include <math_constants.h>
 
 #include <cstdint>
@@ -80,7 +86,9 @@ constexpr uint32_t kIdescDqRope = idesc_f32acc(64, 64, 1, 1, kFmtBf16);
 constexpr uint32_t kIdescKv = idesc_f32acc(128, 64, 1, 0, kFmtBf16);
 constexpr uint32_t kIdescKvRope = idesc_f32acc(64, 64, 1, 0, kFmtBf16);
 
-// The part of one row-set that this CTA walks: live tiles j0 .. j1 - 1 (none when j0 >= j1).
+// The part of one row-set that this CTA walks: live tiles j0 .. j1 - 1 (none when j0 >= j1), starting
+// `turn` tiles in and wrapping round. Lists are usually ascending, so that CTAs in step would all
+// add to the same few cache rows at a time; each CTA starts at another place of the list.
 struct Seg {
   int rowset, t;
   long long base;  // first of its rows in [T * H, ...]
@@ -88,6 +96,12 @@ struct Seg {
   int j0, j1;
   bool whole;      // this CTA has every tile of the row-set
   int part;        // where its dq goes otherwise
+  int turn;
+  // The i-th tile walked.
+  __device__ int tile(int i) const {
+    const int j = i + turn;
+    return j < j1 ? j : j - (j1 - j0);
+  }
 };
 
 // Walks the segments of CTA blockIdx.x; every role runs its own copy.
@@ -111,6 +125,7 @@ struct SegIter {
     const int live = (p.live_len[s.t] + kEntries - 1) / kEntries;
     s.j0 = static_cast<int>(pos - first);
     s.j1 = min(static_cast<int>(end - first), live);
+    s.turn = s.j0 < s.j1 ? static_cast<int>(static_cast<long long>(blockIdx.x) * (s.j1 - s.j0) / p.num_ctas) : 0;
     s.whole = pos == first && end == first + p.tiles;
     s.part = static_cast<int>(streamk_part_slot(blockIdx.x, first, p.total_tiles, p.num_ctas));
     pos = end;
@@ -152,7 +167,7 @@ __device__ __forceinline__ void gather_role(const BackwardParams& p, uint8_t* sm
         slot[i] = r < kEntries && k < p.K ? __ldg(list + k) : -1;
       }
     };
-    load_slots(s.j0);
+    load_slots(s.tile(s.j0));
     for (int j = s.j0; j < s.j1; ++j, ++g) {
       if (j > s.j0) mbar_wait(bar(kBarKvFree), (g - 1) & 1, wc);
 #pragma unroll
@@ -166,7 +181,7 @@ __device__ __forceinline__ void gather_role(const BackwardParams& p, uint8_t* sm
         for (int kb = 0; kb < 9; ++kb) cp_async16(at + kb * kBlk, row + 128 * kb, ok);
         if (c == 0) misc->slot[g & 3][r] = slot[i];
       }
-      if (j + 1 < s.j1) load_slots(j + 1);
+      if (j + 1 < s.j1) load_slots(s.tile(j + 1));
       cp_async_wait_all();
       fence_proxy_async_smem();  // the rows (generic proxy) -> MMA operand reads
       if (!(g == 0 && (p.fault & kFaultWithholdFirstFill))) mbar_arrive(bar(kBarKvFull));
@@ -175,9 +190,25 @@ __device__ __forceinline__ void gather_role(const BackwardParams& p, uint8_t* sm
   }
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+// Four MMAs of K = 16 each, or the first `steps` of them: a and b are the first one's descriptors,
+// which advance by kA and kB bytes.
+template <uint32_t kIdesc, uint32_t kA, uint32_t kB>
+__device__ __forceinline__ void umma_x4(uint32_t d, uint64_t a, uint64_t b, bool accumulate, int steps = 4) {
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks)
+    if (ks < steps) umma_f16(d, a + ((ks * kA) >> 4), b + ((ks * kB) >> 4), kIdesc, ks > 0 || accumulate);
+}
+
 // The one thread that issues the MMAs. Per tile: dq (which frees the rows' tile), four blocks of dKV
-// while the next rows land, the next tile's S^T and dP^T, the last block. A descriptor is a base plus a constant: computed anew for each MMA, the issue took longer than the
-// product (80 cycles each).
+// while the next rows land, the next tile's S^T and dP^T, the last block. The issue has to keep up
+// with products of 32 to 64 cycles: one elected lane of a uniform warp (a lane chosen by its number:
+// 70 cycles an MMA, elected: 45), descriptors that advance by constants, loops of a few MMAs.
 __device__ __forceinline__ void mma_role(const BackwardParams& p, uint8_t* smem, uint32_t tmem, uint32_t bars,
                                          const WaitCtl& wc) {
   const uint32_t base = smem_u32(smem);
@@ -193,33 +224,13 @@ __device__ __forceinline__ void mma_role(const BackwardParams& p, uint8_t* smem,
     if (g > 0 && !(mbar_wait(bar(kBarBlockFree + 1), (g - 1) & 1, wc) && mbar_wait(bar(kBarBlockFree + 3), (g - 1) & 1, wc)))
       return false;
     tc_fence_after();
-#pragma unroll
-    for (int kb = 0; kb < 8; ++kb)
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-        umma_f16(tmem + kTmS, kv_k + ((kb * kBlk + ks * 32) >> 4), q_k + ((2 * kb * kBlk + ks * 32) >> 4), kIdescS,
-                 (kb | ks) != 0);
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
-      umma_f16(tmem + kTmS, kv_k + ((8 * kBlk + ks * 32) >> 4), q_k + ((16 * kBlk + ks * 32) >> 4), kIdescSRope, 1);
+#pragma unroll 1
+    for (uint32_t kb = 0; kb < 8; ++kb)
+      umma_x4<kIdescS, 32, 32>(tmem + kTmS, kv_k + kb * (kBlk >> 4), q_k + kb * (2 * kBlk >> 4), kb > 0);
+    umma_x4<kIdescSRope, 32, 32>(tmem + kTmS, kv_k + 8 * (kBlk >> 4), q_k + 16 * (kBlk >> 4), true);
     umma_commit(bar(kBarS));
     return true;
   };
-  // block cb of dKV^T into columns d
-  auto block = [&](auto cbc, uint32_t d) {
-    constexpr int cb = decltype(cbc)::value;
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
-      umma_f16(d, q_mn + ((4 * cb * kBlk + ks * 2048) >> 4), ds_k + ((ks * 32) >> 4), cb < 4 ? kIdescKv : kIdescKvRope,
-               ks > 0);
-    if constexpr (cb < 4) {
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-        umma_f16(d, q_mn + (((4 * cb + 1) * kBlk + ks * 2048) >> 4), p_k + ((ks * 32) >> 4), kIdescKv, 1);
-    }
-    umma_commit(bar(kBarBlock + cb));
-  };
-  using std::integral_constant;
   uint32_t g = 0;
   bool ok = true;
   SegIter it(p);
@@ -227,30 +238,35 @@ __device__ __forceinline__ void mma_role(const BackwardParams& p, uint8_t* smem,
   while (ok && it.next(s)) {
     if (s.j0 >= s.j1) continue;
     ok = scores(g);
+    const int steps = (s.nvalid + 15) / 16;  // rows past the last head add nothing to dKV
     for (int j = s.j0; ok && j < s.j1; ++j, ++g) {
       ok = mbar_wait(bar(kBarP), g & 1, wc);
       if (ok && j == s.j0 && segs > 0) ok = mbar_wait(bar(kBarDqFree), (segs - 1) & 1, wc);
       if (!ok) break;
       tc_fence_after();
-#pragma unroll
-      for (int mb = 0; mb < 5; ++mb)
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          umma_f16(tmem + kTmDq + 64 * mb, kv_mn + ((2 * mb * kBlk + ks * 2048) >> 4), ds_mn + ((ks * 2048) >> 4),
-                   mb < 4 ? kIdescDq : kIdescDqRope, j > s.j0 || ks > 0);
+#pragma unroll 1
+      for (uint32_t mb = 0; mb < 4; ++mb)
+        umma_x4<kIdescDq, 2048, 2048>(tmem + kTmDq + 64 * mb, kv_mn + mb * (2 * kBlk >> 4), ds_mn, j > s.j0);
+      umma_x4<kIdescDqRope, 2048, 2048>(tmem + kTmDq + 256, kv_mn + 8 * (kBlk >> 4), ds_mn, j > s.j0);
       umma_commit(bar(kBarKvFree));
-      block(integral_constant<int, 0>{}, tmem + kTmS);
-      block(integral_constant<int, 1>{}, tmem + kTmDp);
-      if (g > 0 && !(ok = mbar_wait(bar(kBarBlockFree + 4), (g - 1) & 1, wc))) break;
+#pragma unroll 1
+      for (uint32_t cb = 0; cb < 4; ++cb) {
+        // what the block's columns held before has been read
+        if (cb == 2 && g > 0) ok = mbar_wait(bar(kBarBlockFree + 4), (g - 1) & 1, wc);
+        if (cb == 3) ok = mbar_wait(bar(kBarBlockFree), g & 1, wc);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (cb == 1 ? kTmDp : (cb == 2 ? kTmX : kTmS));
+        umma_x4<kIdescKv, 2048, 32>(d, q_mn + cb * (4 * kBlk >> 4), ds_k, false, steps);
+        umma_x4<kIdescKv, 2048, 32>(d, q_mn + cb * (4 * kBlk >> 4) + (kBlk >> 4), p_k, true, steps);
+        umma_commit(bar(kBarBlock + static_cast<int>(cb)));
+      }
+      if (ok && j + 1 < s.j1) ok = scores(g + 1);
+      if (ok) ok = mbar_wait(bar(kBarBlockFree + 2), g & 1, wc);
+      if (!ok) break;
       tc_fence_after();
-      block(integral_constant<int, 2>{}, tmem + kTmX);
-      if (!(ok = mbar_wait(bar(kBarBlockFree), g & 1, wc))) break;
-      tc_fence_after();
-      block(integral_constant<int, 3>{}, tmem + kTmS);
-      if (j + 1 < s.j1 && !(ok = scores(g + 1))) break;
-      if (!(ok = mbar_wait(bar(kBarBlockFree + 2), g & 1, wc))) break;
-      tc_fence_after();
-      block(integral_constant<int, 4>{}, tmem + kTmX);
+      umma_x4<kIdescKvRope, 2048, 32>(tmem + kTmX, q_mn + 16 * (kBlk >> 4), ds_k, false, steps);
+      umma_commit(bar(kBarBlock + 4));
       umma_commit(bar(kBarPFree));
     }
     umma_commit(bar(kBarSeg));
@@ -261,15 +277,51 @@ __device__ __forceinline__ void mma_role(const BackwardParams& p, uint8_t* smem,
   mbar_wait_ignoring_abort(bar(kBarDone), 0, wc);  // nothing runs when tensor memory is released
 }
 
-// Adds v[e] to dst of cache row slots[e], e < 32 (the warp's lanes are consecutive channels).
+// The cache rows' sums keep their channels in an order that suits add_rows: each 32 latent channels as
+// 8 x 4 (channels c, c + 8, c + 16, c + 24 side by side), each 16 rope channels as 4 x 4 (c, c + 4, c + 8,
+// c + 12). finish_kernel puts them right.
+
+// Adds v[e] of this lane's channel to cache row slots[e], e < 32; the warp's lanes are 32 consecutive
+// latent channels, or with kRope the lower 16 lanes 16 rope channels; dst is the first one in row 0.
+// Lanes exchange four entries' values (two butterfly steps), after which a lane holds four channels of
+// one entry, 16 consecutive bytes of the sums, and neighbours continue the line: a quarter of the
+// instructions that single additions take.
+template <bool kRope>
 __device__ __forceinline__ void add_rows(float* dst, const int* slots, const uint32_t (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kLow = kRope ? 4 : 8;      // lanes that hold one entry afterwards
+  constexpr int kStep = kRope ? 8 : 4;     // entries per instruction
+  const bool up = (lane & kLow) != 0, top = (lane & (2 * kLow)) != 0;
+  dst += (lane & (kLow - 1)) * 4;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int4 s = reinterpret_cast<const int4*>(slots)[i];
-    if (s.x >= 0) atomicAdd(dst + static_cast<long long>(s.x) * kRow, __uint_as_float(v[4 * i]));
-    if (s.y >= 0) atomicAdd(dst + static_cast<long long>(s.y) * kRow, __uint_as_float(v[4 * i + 1]));
-    if (s.z >= 0) atomicAdd(dst + static_cast<long long>(s.z) * kRow, __uint_as_float(v[4 * i + 2]));
-    if (s.w >= 0) atomicAdd(dst + static_cast<long long>(s.w) * kRow, __uint_as_float(v[4 * i + 3]));
+  for (int i = 0; i < 32; i += kStep) {
+    uint32_t x[4] = {v[i], v[i + 1], v[i + 2], v[i + 3]};
+    if constexpr (kRope) {
+      // the upper lanes hold nothing: they take entries i + 4 .. i + 7
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t o = __shfl_sync(0xffffffffu, v[i + 4 + u], lane & 15);
+        if (lane >= 16) x[u] = o;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; u += 2) {
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, up ? x[u] : x[u + 1], kLow);
+      if (up) x[u] = o;
+      else x[u + 1] = o;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, top ? x[u] : x[u + 2], 2 * kLow);
+      if (top) x[u] = o;
+      else x[u + 2] = o;
+    }
+    const int slot = slots[i + (lane / kLow)];
+    if (slot >= 0)
+      asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst + static_cast<long long>(slot) * kRow),
+                   "f"(__uint_as_float(x[0])), "f"(__uint_as_float(x[1])), "f"(__uint_as_float(x[2])),
+                   "f"(__uint_as_float(x[3]))
+                   : "memory");
   }
 }
 
@@ -302,15 +354,15 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
       lse2[i] = v.x;
       delta[i] = v.y * p.scale;
     }
-    // the second half leaves its sums in shared memory, the first adds them a tile later, when the
-    // barriers between have made them visible
+    // the second half leaves its sums in shared memory; the first adds them once the tile's first block of
+    // dKV is there, which the MMAs began when both had arrived
     float held = 0.f;
     bool held_live = false;
     auto put_weight = [&](int j) {
-      const int k = j * kEntries + we;
+      const int k = s.tile(j) * kEntries + we;
       if (half == 0 && pair < 2 && held_live && k < p.K) {
         float* dst = p.weights + static_cast<long long>(s.t) * p.K + k;
-        const float w = held + misc->weight[(g - 1) & 1][we];
+        const float w = held + misc->weight[g & 1][we];
         // two head chunks add to a zero: the same sum in either order
         if (p.hchunks > 1) atomicAdd(dst, w);
         else *dst = w;
@@ -323,7 +375,6 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
       tmem_ld_16x256b_x4(lanes + kTmS + 32 * half, sv);
       tmem_ld_16x256b_x4(lanes + kTmDp + 32 * half, dv);
       const bool live0 = misc->slot[g & 3][e] >= 0, live8 = misc->slot[g & 3][e + 8] >= 0;
-      if (p.weights != nullptr && j > s.j0) put_weight(j - 1);
       tmem_ld_wait();
       uint32_t pp[8], pd[8];  // [2 k]: entry e, [2 k + 1]: entry e + 8
       float w0 = 0.f, w8 = 0.f;
@@ -369,20 +420,20 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
 #pragma unroll 1
       for (int cb = 0; cb < 4; cb += 3) {
         if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarBlock + cb), g & 1, wc))) break;
+        if (cb == 0 && p.weights != nullptr) put_weight(j);
         tc_fence_after();
         uint32_t v[32];
         tmem_ld32(lanes + kTmS + 32 * half, v);
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(bar(kBarBlockFree + cb));
-        add_rows(p.dkv_acc + 128 * cb + 32 * quad + lane, misc->slot[g & 3] + 32 * half, v);
+        add_rows<false>(p.dkv_acc + 128 * cb + 32 * quad, misc->slot[g & 3] + 32 * half, v);
       }
     }
     // dq^T: lane = channel, this warp's heads 32 half .. + 31
     if (any) {
       mbar_wait(bar(kBarDq), segs & 1, wc);
       tc_fence_after();
-      if (p.weights != nullptr) put_weight(s.j1 - 1);
     }
 #pragma unroll 1
     for (int mb = 0; mb < 5; ++mb) {
@@ -439,10 +490,14 @@ __device__ __forceinline__ void scatter_role(const BackwardParams& p, Misc* misc
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(bar(kBarBlockFree + cb));
-        if (cb == 4 && lane >= 16) continue;
-        float* dst = p.dkv_acc + 128 * cb + (cb < 4 ? 32 : 16) * quad + lane;
-        add_rows(dst, misc->slot[g & 3], v[0]);
-        add_rows(dst, misc->slot[g & 3] + 32, v[1]);
+        const int* slots = misc->slot[g & 3];
+        if (cb < 4) {
+          add_rows<false>(p.dkv_acc + 128 * cb + 32 * quad, slots, v[0]);
+          add_rows<false>(p.dkv_acc + 128 * cb + 32 * quad, slots + 32, v[1]);
+        } else {
+          add_rows<true>(p.dkv_acc + kVdim + 16 * quad, slots, v[0]);
+          add_rows<true>(p.dkv_acc + kVdim + 16 * quad, slots + 32, v[1]);
+        }
       }
     }
   }
@@ -452,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const BackwardPar
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Misc* misc = reinterpret_cast<Misc*>(smem + kOffMisc);
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // a uniform value
   const uint32_t bars = smem_u32(misc->bars);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
@@ -481,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const BackwardPar
     scatter_role(p, misc, tmem, bars, wc);
   } else if (warp < kMmaWarp) {
     gather_role(p, smem, misc, bars, wc);
-  } else if ((threadIdx.x & 31) == 0) {
+  } else if (elect_one()) {
     mma_role(p, smem, tmem, bars, wc);
   }
   tc_fence_before();
@@ -490,55 +545,89 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const BackwardPar
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// One CTA per query: its list's cache rows and how far the live ones reach, and per head
-// (lse in log2 units, delta). A head without a live entry (lse = -inf) gets +inf: P = 0.
+// CTAs 0 .. T - 1: a query's list as cache rows, and how far the live ones reach. The next delta_ctas,
+// 32 heads of any queries each: (lse in log2 units, delta); a head without a live entry (lse = -inf)
+// gets +inf, so that P = 0. The others zero the cache rows' sums.
 constexpr int kPrepThreads = 256;
-__global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const BackwardParams p, const ListParams l) {
-  __shared__ int reach;
-  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
-  if (tid == 0) reach = 0;
-  __syncthreads();
-  const ReqContext ctx = request_context(t, l.req_of_token, l.block_table, l.num_reqs, l.max_blocks, l.seq_lens);
-  const int len = l.topk_len ? l.topk_len[t] : p.K;
-  int err = 0, last = 0;
-  for (int k = tid; k < p.K; k += kPrepThreads) {
-    const long long at = static_cast<long long>(t) * p.K + k;
-    int slot = -1;
-    if (k < len) {
-      const int pos = __ldg(l.topk + at);
-      slot = slot_of(pos, page_of(pos, ctx, l.max_blocks, l.page_size), ctx, l.block_table != nullptr, l.max_blocks,
-                     l.page_size, l.num_pages, &err);
+constexpr int kPrepHeads = 32;
+__global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const BackwardParams p, const ListParams l,
+                                                               int delta_ctas) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (static_cast<int>(blockIdx.x) < p.T) {
+    __shared__ int reach;
+    const int t = blockIdx.x;
+    if (tid == 0) reach = 0;
+    __syncthreads();
+    const ReqContext ctx = request_context(t, l.req_of_token, l.block_table, l.num_reqs, l.max_blocks, l.seq_lens);
+    const int len = l.topk_len ? l.topk_len[t] : p.K;
+    int err = 0, last = 0;
+#pragma unroll 4
+    for (int k = tid; k < p.K; k += kPrepThreads) {
+      const long long at = static_cast<long long>(t) * p.K + k;
+      int slot = -1;
+      if (k < len) {
+        const int pos = __ldg(l.topk + at);
+        slot = slot_of(pos, page_of(pos, ctx, l.max_blocks, l.page_size), ctx, l.block_table != nullptr, l.max_blocks,
+                       l.page_size, l.num_pages, &err);
+      }
+      p.slots[at] = slot;
+      if (p.weights != nullptr) p.weights[at] = 0.f;
+      if (slot >= 0) last = k + 1;
     }
-    p.slots[at] = slot;
-    if (p.weights != nullptr) p.weights[at] = 0.f;
-    if (slot >= 0) last = k + 1;
+    last = __reduce_max_sync(0xffffffffu, last);
+    if (lane == 0 && last > 0) atomicMax(&reach, last);
+    if (__any_sync(0xffffffffu, err != 0) && lane == 0) atomicOr(p.status, SVT_DEV_ERR_INDEX_RANGE);
+    __syncthreads();
+    if (tid == 0) p.live_len[t] = reach;
+    return;
   }
-  last = __reduce_max_sync(0xffffffffu, last);
-  if (lane == 0 && last > 0) atomicMax(&reach, last);
-  if (__any_sync(0xffffffffu, err != 0) && lane == 0) atomicOr(p.status, SVT_DEV_ERR_INDEX_RANGE);
-  for (int h = tid >> 5; h < p.H; h += kPrepThreads / 32) {
-    const long long r = static_cast<long long>(t) * p.H + h;
-    float d = 0.f;
+  const int cta = blockIdx.x - p.T;
+  if (cta >= delta_ctas) {
+    const long long n = p.num_slots * (kRow / 4), step = (gridDim.x - p.T - delta_ctas) * static_cast<long long>(kPrepThreads);
+    for (long long i = (cta - delta_ctas) * static_cast<long long>(kPrepThreads) + tid; i < n; i += step)
+      reinterpret_cast<float4*>(p.dkv_acc)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    return;
+  }
+  // a warp takes two heads at a time: eight 16-byte loads in flight a lane
+  const long long rows = static_cast<long long>(p.T) * p.H;
+#pragma unroll 1
+  for (int i = 0; i < kPrepHeads; i += 2 * kPrepThreads / 32) {
+    const long long r0 = static_cast<long long>(cta) * kPrepHeads + i + 2 * (tid >> 5);
+    if (r0 >= rows) break;
+    const int count = r0 + 1 < rows ? 2 : 1;
+    uint4 a[2][2], b[2][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(p.out + r * kVdim) + lane + 32 * i);
-      const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.dout + r * kVdim) + lane + 32 * i);
-      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+    for (int u = 0; u < 2; ++u)
+      if (u < count) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        d = fmaf(__uint_as_float(aw[k] << 16), __uint_as_float(bw[k] << 16), d);
-        d = fmaf(__uint_as_float(aw[k] & 0xFFFF0000u), __uint_as_float(bw[k] & 0xFFFF0000u), d);
+        for (int k = 0; k < 2; ++k) {
+          a[u][k] = __ldg(reinterpret_cast<const uint4*>(p.out + (r0 + u) * kVdim) + lane + 32 * k);
+          b[u][k] = __ldg(reinterpret_cast<const uint4*>(p.dout + (r0 + u) * kVdim) + lane + 32 * k);
+        }
+      }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (u >= count) break;
+      const long long r = r0 + u;
+      float d = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t aw[4] = {a[u][k].x, a[u][k].y, a[u][k].z, a[u][k].w};
+        const uint32_t bw[4] = {b[u][k].x, b[u][k].y, b[u][k].z, b[u][k].w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          d = fmaf(__uint_as_float(aw[w] << 16), __uint_as_float(bw[w] << 16), d);
+          d = fmaf(__uint_as_float(aw[w] & 0xFFFF0000u), __uint_as_float(bw[w] & 0xFFFF0000u), d);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+      if (lane == 0) {
+        const float lse = p.lse[r];
+        p.stats[r] = make_float2(lse == -CUDART_INF_F ? CUDART_INF_F : lse * kLog2e, d - (p.dlse ? p.dlse[r] : 0.f));
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if (lane == 0) {
-      const float lse = p.lse[r];
-      p.stats[r] = make_float2(lse == -CUDART_INF_F ? CUDART_INF_F : lse * kLog2e, d - (p.dlse ? p.dlse[r] : 0.f));
-    }
   }
-  __syncthreads();
-  if (tid == 0) p.live_len[t] = reach;
 }
 
 // CTAs below join_ctas join the dq of the row-set that the border before CTA c + 1 of the main
@@ -576,12 +665,31 @@ __global__ void __launch_bounds__(256) finish_kernel(const BackwardParams p, int
     }
     return;
   }
-  const long long n8 = p.num_slots * (kRow / 8), step = (gridDim.x - join_ctas) * 256ll;
-  for (long long i = (blockIdx.x - join_ctas) * 256ll + threadIdx.x; i < n8; i += step) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p.dkv_acc) + 2 * i);
-    const float4 b = __ldcs(reinterpret_cast<const float4*>(p.dkv_acc) + 2 * i + 1);
-    reinterpret_cast<uint4*>(p.dkv)[i] = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w),
-                                                    pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+  // a thread takes 32 channels, in the order of add_rows: eight 16-byte reads, four 16-byte writes
+  const long long n = p.num_slots * (kRow / 32), step = (gridDim.x - join_ctas) * 256ll;
+  for (long long i = (blockIdx.x - join_ctas) * 256ll + threadIdx.x; i < n; i += step) {
+    float4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = reinterpret_cast<const float4*>(p.dkv_acc)[8 * i + k];
+    uint4* dst = reinterpret_cast<uint4*>(p.dkv) + 4 * i;
+    if (i % (kRow / 32) < kVdim / 32) {
+      dst[0] = make_uint4(pack_bf16x2(v[0].x, v[1].x), pack_bf16x2(v[2].x, v[3].x), pack_bf16x2(v[4].x, v[5].x),
+                          pack_bf16x2(v[6].x, v[7].x));
+      dst[1] = make_uint4(pack_bf16x2(v[0].y, v[1].y), pack_bf16x2(v[2].y, v[3].y), pack_bf16x2(v[4].y, v[5].y),
+                          pack_bf16x2(v[6].y, v[7].y));
+      dst[2] = make_uint4(pack_bf16x2(v[0].z, v[1].z), pack_bf16x2(v[2].z, v[3].z), pack_bf16x2(v[4].z, v[5].z),
+                          pack_bf16x2(v[6].z, v[7].z));
+      dst[3] = make_uint4(pack_bf16x2(v[0].w, v[1].w), pack_bf16x2(v[2].w, v[3].w), pack_bf16x2(v[4].w, v[5].w),
+                          pack_bf16x2(v[6].w, v[7].w));
+    } else {
+#pragma unroll
+      for (int h = 0; h < 8; h += 4) {
+        dst[h / 2] = make_uint4(pack_bf16x2(v[h].x, v[h + 1].x), pack_bf16x2(v[h + 2].x, v[h + 3].x),
+                                pack_bf16x2(v[h].y, v[h + 1].y), pack_bf16x2(v[h + 2].y, v[h + 3].y));
+        dst[h / 2 + 1] = make_uint4(pack_bf16x2(v[h].z, v[h + 1].z), pack_bf16x2(v[h + 2].z, v[h + 3].z),
+                                    pack_bf16x2(v[h].w, v[h + 1].w), pack_bf16x2(v[h + 2].w, v[h + 3].w));
+      }
+    }
   }
 }
 
@@ -595,24 +703,26 @@ void plan_backward(BackwardParams& p, int sms) {
 }
 
 cudaError_t launch_backward(const BackwardParams& p, const ListParams& l, cudaStream_t stream) {
-  cudaError_t e = cudaMemsetAsync(p.dkv_acc, 0, static_cast<size_t>(p.num_slots) * kRow * sizeof(float), stream);
-  if (e != cudaSuccess) return e;
-  int join = 0;
-  if (p.total_tiles > 0) {
-    e = cudaFuncSetAttribute(backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    prepare_kernel<<<static_cast<unsigned>(p.T), kPrepThreads, 0, stream>>>(p, l);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    backward_kernel<<<static_cast<unsigned>(p.num_ctas), kThreads, kSmem, stream>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    join = (p.num_ctas - 1) * (kRows / kJoinRows);
-  } else if (p.T > 0) {
+  cudaError_t e = cudaSuccess;
+  const bool any = p.total_tiles > 0;
+  if (!any && p.T > 0) {  // empty lists: no gradient
     e = cudaMemsetAsync(p.dq, 0, static_cast<size_t>(p.T) * p.H * kRow * sizeof(uint16_t), stream);
     if (e != cudaSuccess) return e;
   }
-  const long long n = (p.num_slots * (kRow / 8) + 255) / 256;
+  if (!any) return cudaMemsetAsync(p.dkv, 0, static_cast<size_t>(p.num_slots) * kRow * sizeof(uint16_t), stream);
+  e = cudaFuncSetAttribute(backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  const long long zero = (p.num_slots * (kRow / 4) + kPrepThreads - 1) / kPrepThreads;
+  const int delta_ctas = static_cast<int>((static_cast<long long>(p.T) * p.H + kPrepHeads - 1) / kPrepHeads);
+  prepare_kernel<<<static_cast<unsigned>(p.T + delta_ctas + (zero < 1216 ? zero : 1216)), kPrepThreads, 0, stream>>>(
+      p, l, delta_ctas);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  backward_kernel<<<static_cast<unsigned>(p.num_ctas), kThreads, kSmem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int join = (p.num_ctas - 1) * (kRows / kJoinRows);
+  const long long n = (p.num_slots * (kRow / 32) + 255) / 256;
   finish_kernel<<<static_cast<unsigned>(join + (n < 1216 ? n : 1216)), 256, 0, stream>>>(p, join);
   return cudaGetLastError();
 }
