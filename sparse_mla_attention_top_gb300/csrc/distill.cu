@@ -3,9 +3,12 @@
 //   p = the list's values normalised (weights), or softmax(value / tau) (logits),
 //   q = softmax(x / tau) over all candidates, or over the listed ones,
 //   loss = sum_j p_j (ln p_j - ln q_j),   d loss / d x_n = (q_n - sum of p at n) / tau.
-// With W = sum w, A = sum w ln w, B = sum w x / tau and the student's normaliser lse (natural
-// log): loss = A / W - ln W - B / W + lse, so one sweep over the list serves the loss. Everything
-// runs in log2 units, exponents relative to the row's largest score.
+// Everything runs in log2 units (c = log2(e) / tau), exponents relative to the row's largest score. With
+// weights w, W = sum w, and the student's normaliser L = log2 sum 2^(c x):
+//   weights: loss = sum w (log2 w - c x) / W - log2 W + L,
+//   logits:  loss = sum w (c value - c x) / W - c max - log2 W + L,  w = 2^(c (value - max)),
+// so one sweep over the list serves the loss; an entry's two logarithms are subtracted before they
+// are summed, which keeps a small loss of long logarithms.
 //
 // Bound: reading the scores once and writing the gradient once. A row is cut between the CTAs
 // of a cluster so that each part (up to 64 KB) stays in shared memory: it is read from memory
@@ -33,8 +36,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxSplit = 8;
 
 struct Stats {
-  float m, s;     // largest score, sum of 2^(c (x - m)) (this CTA's candidates)
-  float w, a, b;  // sums of w, w log2 w and w c x (this CTA's share of the list)
+  float m, s;  // largest score, sum of 2^(c (x - m)) (this CTA's candidates)
+  float w, d;  // sums of w and of w e (this CTA's share of the list), e as below
 };
 
 struct DistillShared {
@@ -42,27 +45,35 @@ struct DistillShared {
   Stats stats[kMaxSplit];  // every CTA's, pushed by each
 };
 
-// Four values over the block: sums, or with kMax maxima. One barrier; `red` alternates between
-// calls, so that a slow warp still reads the previous array.
+// Three sums over the block (x, y, z), or with kMax two maxima (x, y; NaN ignored). One barrier; `red`
+// alternates between calls, so that a slow warp still reads the previous array.
 template <bool kMax>
 __device__ __forceinline__ float4 block_reduce(float4 v, float4* red) {
-  auto op = [](float x, float y) { return kMax ? fmaxf(x, y) : x + y; };
-  auto step = [&](int o) {
-    v.x = op(v.x, __shfl_xor_sync(0xffffffffu, v.x, o));
-    v.y = op(v.y, __shfl_xor_sync(0xffffffffu, v.y, o));
-    if (!kMax) {
-      v.z = op(v.z, __shfl_xor_sync(0xffffffffu, v.z, o));
-      v.w = op(v.w, __shfl_xor_sync(0xffffffffu, v.w, o));
+  const int lane = threadIdx.x & 31;
+  auto over = [&](float4 q) {
+    if constexpr (kMax) {
+      q.x = warp_max_f32(q.x);
+      q.y = warp_max_f32(q.y);
+    } else {
+      // the halves of the warp take x and y; z goes along
+      const bool up = (lane & 16) != 0;
+      float a = up ? q.y : q.x;
+      a += __shfl_xor_sync(0xffffffffu, up ? q.x : q.y, 16);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) q.z += __shfl_xor_sync(0xffffffffu, q.z, o);
+      const float b = __shfl_xor_sync(0xffffffffu, a, 16);
+      q.x = up ? b : a;
+      q.y = up ? a : b;
     }
+    return q;
   };
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) step(o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  v = over(v);
+  if (lane == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = red[threadIdx.x & (kWarps - 1)];
-#pragma unroll
-  for (int o = kWarps / 2; o > 0; o >>= 1) step(o);
-  return v;
+  const float none = kMax ? -CUDART_INF_F : 0.f;
+  return over(lane < kWarps ? red[lane] : make_float4(none, none, none, none));
 }
 
 __device__ __forceinline__ float load1(const float* p) { return __ldg(p); }
@@ -165,7 +176,8 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
   float* part = reinterpret_cast<float*>(dyn);
   __shared__ DistillShared sh;
   auto cl = cooperative_groups::this_cluster();
-  if (p.split > 1) cl.barrier_arrive();  // (completed below) every CTA of the cluster has started
+  // (completed below) every CTA of the cluster has started
+  if (p.split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int tid = threadIdx.x;
   const int t = blockIdx.x / p.split, cr = blockIdx.x - t * p.split;
   const E* row = static_cast<const E*>(p.scores) + static_cast<long long>(t) * p.stride;
@@ -213,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     if (kFit)
       for (int j = tid; j < n; j += kThreads) part[j] = 0.f;
   }
-  Stats st{-CUDART_INF_F, 0.f, 0.f, 0.f, 0.f};
+  Stats st{-CUDART_INF_F, 0.f, 0.f, 0.f};
   if constexpr (kAll && !kFit) {
     for (int a = lo; a < chi; a += kPart) {
       const int m = min(kPart, chi - a);
@@ -249,16 +261,12 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
       if (!mine) return;
       const float w = weight(v);
       r.y += w;
-      if (w != 0.f) {
-        r.z += p.logits ? w * ((v - tmax) * c) : w * log2f(w);
-        r.w += w * (x * c);
-      }
+      if (w != 0.f) r.z += w * (p.logits ? (v - x) * c : fmaf(-x, c, log2f(w)));
     });
     r = block_reduce<false>(r, sh.red[1]);
     if (!(kAll && !kFit)) st.s = r.x;
     st.w = r.y;
-    st.a = r.z;
-    st.b = r.w;
+    st.d = r.z;
   }
   // the listed columns of this CTA as they stand, before any of them changes
   float held_e[kHeld];
@@ -270,16 +278,15 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     }
   }
 
-  float M = st.m, Z = st.s, W = st.w, A = st.a, B = st.b;
+  float M = st.m, Z = st.s, W = st.w, D = st.d;
   if (p.split > 1) {
-    cl.barrier_wait();
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if (tid < p.split) cl.map_shared_rank(&sh, static_cast<unsigned>(tid))->stats[cr] = st;
     cl.sync();  // every CTA's statistics are here
-    W = A = B = 0.f;
+    W = D = 0.f;
     for (int r = 0; r < p.split; ++r) {
       W += sh.stats[r].w;
-      A += sh.stats[r].a;
-      B += sh.stats[r].b;
+      D += sh.stats[r].d;
     }
     if constexpr (kAll) {
       M = -CUDART_INF_F;
@@ -306,7 +313,8 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     double inv = static_cast<double>(1.f / W);
     if (W > 1e-30f && W < 1e30f) inv = inv * (2.0 - W * inv);
     else inv = 1.0 / W;
-    const double d = (static_cast<double>(A) - static_cast<double>(B)) * inv + static_cast<double>(top) +
+    const double d = static_cast<double>(D) * inv + static_cast<double>(top) -
+                     (p.logits ? static_cast<double>(tmax) * static_cast<double>(c) : 0.0) +
                      static_cast<double>(ez - ew) + (static_cast<double>(log2f(mz)) - static_cast<double>(log2f(mw)));
     p.loss[t] = some ? static_cast<float>(d * 0.69314718055994530942) : 0.f;
   }
