@@ -165,15 +165,20 @@ class KVCache:
 
 class Workspace:
     """Caller-owned scratch for one stream: a 256-byte status header plus per-call space.
-    Grows on demand (allocation happens here, in torch, never inside the library)."""
+    Grows on demand (allocation happens here, in torch, never inside the library). Outgrown buffers
+    are kept: a captured graph goes on using the one it was captured with (its status bits stay there),
+    so size a workspace before the capture where they are to be read."""
 
     def __init__(self, device=None, nbytes: int = 256):
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         self.buf = torch.zeros(max(256, nbytes), dtype=torch.uint8, device=self.device)
+        self._outgrown = []
 
     def ensure(self, nbytes: int) -> "Workspace":
         if nbytes > self.buf.numel():
             old = self.buf
+            nbytes = max(nbytes, old.numel() * 3 // 2)  # so that those kept add up to twice the last
+            self._outgrown.append(old)
             self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
             self.buf[:256].copy_(old[:256])  # keep pending status bits
         return self
@@ -197,9 +202,10 @@ _default_ws = {}
 
 def default_workspace() -> Workspace:
     dev = torch.cuda.current_device()
-    if dev not in _default_ws:
-        _default_ws[dev] = Workspace()
-    return _default_ws[dev]
+    ws = _default_ws.get(dev)
+    if ws is None:
+        ws = _default_ws[dev] = Workspace()
+    return ws
 
 
 def resolve_topk_slots(topk_pos, *, block_table=None, seq_lens=None, req_of_token=None, topk_len=None,
@@ -312,29 +318,25 @@ def topk_select(scores, K: int, *, lens=None, out=None):
     return out
 
 
-# The current stream's handle without building a Stream object (several microseconds a call).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_fast = None
 
 
-def _launch_on(first, **tensors):
-    """The device index and current stream of a launch: `first` is on the current CUDA device
-    (kernels are launched there, on its current stream) and every other given tensor beside it."""
-    dev = first.get_device()
-    if dev < 0 or dev != torch._C._cuda_getDevice():
-        raise TypeError(f"tensors must be on the current CUDA device, not {first.device}")
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != dev:
-            raise TypeError(f"{name} must be on {first.device}, not {t.device}")
-    return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(dev)
-
-
-def _shaped(t, name: str, dtype, shape):
-    """The address of `t`, a contiguous tensor of this type and shape; None for None."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
-    return t.data_ptr()
+def _binding():
+    """The compiled binding (csrc/binding.cpp) of the short calls below, bound to the loaded library. It
+    makes the checks of tensors: types, shapes, and that all are on the current CUDA device."""
+    global _fast
+    if _fast is None:
+        L = lib()
+        try:
+            from . import _binding as fast
+        except ImportError as e:
+            raise RuntimeError("_binding.so is missing or stale: build it first "
+                               "(sparse_mla_attention_top_gb300.build)") from e
+        fast.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.svt_rope, L.svt_rope_append, L.svt_sparse_mla_backward_workspace_size, L.svt_sparse_mla_backward,
+            L.svt_distill_topk)))
+        _fast = fast
+    return _fast
 
 
 def _choice(value: str, choices: dict, name: str) -> int:
@@ -342,24 +344,6 @@ def _choice(value: str, choices: dict, name: str) -> int:
     if code is None:
         raise ValueError(f"{name} must be one of {', '.join(choices)}, got {value!r}")
     return code
-
-
-def _rows3(x, name: str):
-    """x [T, D] or [T, H, D] as (T, H, D, stride t, stride h); unit column stride. A dimension of
-    one row has no meaningful stride."""
-    shape, stride = x.shape, x.stride()
-    if len(shape) == 3:
-        T, H, D = shape
-        st, sh, sd = stride
-    elif len(shape) == 2:
-        T, D = shape
-        st, sd = stride
-        H, sh = 1, D
-    else:
-        raise TypeError(f"{name} must be [T, D] or [T, H, D]")
-    if sd != 1 and D > 1:
-        raise TypeError(f"{name} must have unit column stride")
-    return T, H, D, (st if T > 1 else H * D), (sh if H > 1 else D)
 
 
 def rope_frequencies(dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
@@ -378,22 +362,11 @@ def rope(x, positions, freqs, *, offset: int = 0, layout: str = "interleaved", i
     """svt_rope: rotates columns offset .. offset + 2 len(freqs) - 1 of x ([T, H, D] or [T, D], bf16
     or fp32, rows may be strided) by its tokens' positions; the other columns are copied. out=x
     rotates in place. inverse=True turns back: it maps the gradient of the result to x's."""
-    dtype = x.dtype
-    if dtype != torch.bfloat16 and dtype != torch.float32:
-        raise TypeError("x must be bf16 or fp32")
-    T, H, D, xt, xh = _rows3(x, "x")
-    if out is None:
-        out = torch.empty(x.shape, dtype=dtype, device=x.device)
-    elif out.dtype != dtype or out.shape != x.shape:
-        raise TypeError("out must have x's type and shape")
-    _, _, _, ot, oh = _rows3(out, "out")
-    pairs = freqs.numel()
-    at, fr = _shaped(positions, "positions", torch.int32, (T,)), _shaped(freqs, "freqs", torch.float64, (pairs,))
-    stream = _launch_on(x, positions=positions, freqs=freqs, out=out)
-    _check(lib().svt_rope(x.data_ptr(), out.data_ptr(), 1 if dtype == torch.float32 else 0, T, H, D, xt, xh, ot, oh, at,
-                          fr, 2 * pairs, offset, _choice(layout, ROPE_LAYOUTS, "layout"), amplitude,
-                          1 if inverse else 0, stream), "svt_rope")
-    return out
+    r = (_fast or _binding()).rope(x, positions, freqs, offset, _choice(layout, ROPE_LAYOUTS, "layout"), inverse, amplitude,
+                                   out)
+    if type(r) is int:
+        _check(r, "svt_rope")
+    return r
 
 
 def rope_append(latent, k_rope, positions, slots, kv: KVCache, freqs, *, layout: str = "interleaved",
@@ -402,46 +375,13 @@ def rope_append(latent, k_rope, positions, slots, kv: KVCache, freqs, *, layout:
     strided) to cache rows slots [T] (negative: skipped); with q_rope [T, H, 64] it rotates the
     queries' rope columns into q_out (a new tensor when None; q[..., 512:] of a [T, H, 576] q fits)
     in the same launch. Returns q_out."""
-    bf16 = torch.bfloat16
-    for name, t, width in (("latent", latent, 512), ("k_rope", k_rope, 64)):
-        if t.dtype != bf16 or t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1:
-            raise TypeError(f"{name} must be a bf16 [T, {width}] tensor with unit column stride")
-    T = latent.shape[0]
-    if k_rope.shape[0] != T:
-        raise TypeError("latent and k_rope must have the same number of rows")
-    at, sl = _shaped(positions, "positions", torch.int32, (T,)), _shaped(slots, "slots", torch.int32, (T,))
-    fr = _shaped(freqs, "freqs", torch.float64, (32,))
-    qi = qo = None
-    H = qt = qh = ot = oh = 0
-    if q_rope is not None:
-        if q_out is None:
-            q_out = torch.empty(q_rope.shape, dtype=bf16, device=q_rope.device)
-        if q_rope.dtype != bf16 or q_rope.dim() != 3 or q_rope.shape[0] != T or q_rope.shape[2] != 64:
-            raise TypeError("q_rope must be a bf16 [T, H, 64] tensor")
-        if q_out.dtype != bf16 or q_out.shape != q_rope.shape:
-            raise TypeError("q_out must have q_rope's type and shape")
-        _, H, _, qt, qh = _rows3(q_rope, "q_rope")
-        _, _, _, ot, oh = _rows3(q_out, "q_out")
-        if H > 0:
-            qi, qo = q_rope.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise TypeError("q_out needs q_rope")
-    stream = _launch_on(latent, k_rope=k_rope, positions=positions, slots=slots, kv=kv.data, freqs=freqs,
-                        q_rope=q_rope, q_out=q_out)
-    _cache_fits(kv)
-    ws = default_workspace() if ws is None else ws
-    _check(lib().svt_rope_append(latent.data_ptr(), latent.stride(0) if T > 1 else 512, k_rope.data_ptr(),
-                                 k_rope.stride(0) if T > 1 else 64, at, sl, T, ctypes.byref(kv._c()), fr,
-                                 _choice(layout, ROPE_LAYOUTS, "layout"), amplitude, qi, H, qt, qh, qo, ot, oh,
-                                 ws.buf.data_ptr(), ws.buf.numel(), stream), "svt_rope_append")
-    return q_out
-
-
-def _cache_fits(kv: KVCache) -> None:
-    """The cache's tensor holds the rows its descriptor promises."""
-    row = ROW_BYTES.get(kv.dtype, 0)
-    if kv.data.nbytes < (kv.num_pages * kv.page_size - 1) * (kv.row_stride_bytes or row) + row:
-        raise TypeError("kv data is smaller than num_pages * page_size rows")
+    ws = ws or default_workspace()
+    r = (_fast or _binding()).rope_append(latent, k_rope, positions, slots, kv.data, kv.num_pages, kv.page_size,
+                                          kv.row_stride_bytes, kv.dtype, freqs, _choice(layout, ROPE_LAYOUTS, "layout"),
+                                          amplitude, q_rope, q_out, ws.buf)
+    if type(r) is int:
+        _check(r, "svt_rope_append")
+    return r
 
 
 def sparse_mla_backward(q, kv: KVCache, topk, softmax_scale: float, out, lse, dout, *, dlse=None, block_table=None,
@@ -450,36 +390,17 @@ def sparse_mla_backward(q, kv: KVCache, topk, softmax_scale: float, out, lse, do
     """svt_sparse_mla_backward: the gradients of sparse_mla_decode (or of a grouped prefill, with each
     query's own list). out and lse are the forward's; dout (and dlse) their gradients. Returns
     (dq [T, H, 576] bf16, dkv [num_slots, 576] bf16, weights [T, K] fp32 or None)."""
-    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
-    if q.dtype != bf16 or q.dim() != 3 or q.shape[2] != 576 or not q.is_contiguous():
-        raise TypeError("q must be a contiguous bf16 [T, H, 576] tensor")
-    T, H, _ = q.shape
-    if topk.dim() != 2 or topk.shape[0] != T:
-        raise TypeError("topk must be an int32 [T, K] tensor")
-    K, n = topk.shape[1], kv.num_slots
-    reqs, blocks = (0, 0) if block_table is None else block_table.shape
-    if dq is None:
-        dq = torch.empty((T, H, 576), dtype=bf16, device=q.device)
-    if dkv is None:
-        dkv = torch.empty((n, 576), dtype=bf16, device=q.device)
-    weights = torch.empty((T, K), dtype=f32, device=q.device) if return_weights else None
-    stream = _launch_on(q, kv=kv.data, topk=topk, out=out, lse=lse, dout=dout, dlse=dlse, block_table=block_table,
-                        seq_lens=seq_lens, req_of_token=req_of_token, topk_len=topk_len, dq=dq, dkv=dkv)
-    _cache_fits(kv)
-    L = lib()
-    ws = (ws or default_workspace()).ensure(L.svt_sparse_mla_backward_workspace_size(T, H, K, n))
-    _check(L.svt_sparse_mla_backward(q.data_ptr(), T, H, ctypes.byref(kv._c()),
-                                     _shaped(block_table, "block_table", i32, (reqs, blocks)), reqs, blocks,
-                                     _shaped(req_of_token, "req_of_token", i32, (T,)),
-                                     _shaped(seq_lens, "seq_lens", i32, (reqs,)) if reqs else None,
-                                     _shaped(topk, "topk", i32, (T, K)), K, _shaped(topk_len, "topk_len", i32, (T,)),
-                                     softmax_scale, _shaped(out, "out", bf16, (T, H, 512)),
-                                     _shaped(lse, "lse", f32, (T, H)), _shaped(dout, "dout", bf16, (T, H, 512)),
-                                     _shaped(dlse, "dlse", f32, (T, H)), _shaped(dq, "dq", bf16, (T, H, 576)),
-                                     _shaped(dkv, "dkv", bf16, (n, 576)),
-                                     None if weights is None else weights.data_ptr(), ws.buf.data_ptr(),
-                                     ws.buf.numel(), stream), "svt_sparse_mla_backward")
-    return dq, dkv, weights
+    ws = ws or default_workspace()
+    for _ in range(2):
+        r = (_fast or _binding()).sparse_mla_backward(
+            q, kv.data, kv.num_pages, kv.page_size, kv.row_stride_bytes, kv.dtype, topk, softmax_scale, out, lse, dout, dlse,
+            block_table, seq_lens, req_of_token, topk_len, dq, dkv, return_weights, ws.buf)
+        if type(r) is not int:
+            return r
+        if r >= 0:
+            break
+        ws.ensure(-r)
+    _check(r, "svt_sparse_mla_backward")
 
 
 def distill_topk(scores, topk, teacher, *, lens=None, temperature: float = 1.0, teacher_kind: str = "weights",
@@ -487,30 +408,12 @@ def distill_topk(scores, topk, teacher, *, lens=None, temperature: float = 1.0, 
     """svt_distill_topk: per query, KL(teacher's top entries || softmax of scores) and the gradient of
     row_weight . loss. scores [T, N] fp32 or bf16 (rows may be strided), topk [T, K] positions (-1 =
     none), teacher [T, K] fp32 weights or logits. Returns (loss [T], dscores [T, N] or None)."""
-    dtype, f32, i32 = scores.dtype, torch.float32, torch.int32
-    if (dtype != f32 and dtype != torch.bfloat16) or scores.dim() != 2:
-        raise TypeError("scores must be an fp32 or bf16 [T, N] tensor")
-    T, _, N, stride, _ = _rows3(scores, "scores")
-    if topk.dim() != 2 or topk.shape[0] != T:
-        raise TypeError("topk must be an int32 [T, K] tensor")
-    K = topk.shape[1]
-    loss = torch.empty((T,), dtype=f32, device=scores.device)
-    grad, dstride = None, N
-    if dscores is None and need_grad:
-        dscores = torch.empty((T, N), dtype=dtype, device=scores.device)
-    if dscores is not None:
-        if dscores.dtype != dtype or dscores.shape != scores.shape:
-            raise TypeError("dscores must have scores' type and shape")
-        dstride, grad = _rows3(dscores, "dscores")[3], dscores.data_ptr()
-    stream = _launch_on(scores, topk=topk, teacher=teacher, lens=lens, row_weight=row_weight, dscores=dscores)
-    _check(lib().svt_distill_topk(scores.data_ptr(), 1 if dtype == f32 else 0, T, N, stride,
-                                  _shaped(lens, "lens", i32, (T,)), _shaped(topk, "topk", i32, (T, K)),
-                                  _shaped(teacher, "teacher", f32, (T, K)), K,
-                                  _choice(teacher_kind, TEACHER_KINDS, "teacher_kind"),
-                                  _choice(over, DISTILL_SCOPES, "over"), temperature,
-                                  _shaped(row_weight, "row_weight", f32, (T,)), loss.data_ptr(), grad, dstride, stream),
-           "svt_distill_topk")
-    return loss, dscores
+    r = (_fast or _binding()).distill_topk(scores, topk, teacher, lens, temperature,
+                                           _choice(teacher_kind, TEACHER_KINDS, "teacher_kind"),
+                                           _choice(over, DISTILL_SCOPES, "over"), row_weight, need_grad, dscores)
+    if type(r) is int:
+        _check(r, "svt_distill_topk")
+    return r
 
 
 def debug_pipeline_fault(fault: int = 0, wait_limit_ns: int = 0) -> None:

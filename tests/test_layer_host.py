@@ -163,7 +163,7 @@ def test_distill_refusals(L):
     assert call(T=0, x=None, topk=None, w=None) == svt.SVT_OK
 
 
-def test_bindings_refuse_tensors_the_kernels_cannot_take():
+def test_bindings_refuse_tensors_the_kernels_cannot_take(L):
     x = torch.zeros(2, 3, 64, dtype=torch.bfloat16)
     pos = torch.zeros(2, dtype=torch.int32)
     f = torch.zeros(32, dtype=torch.float64)
