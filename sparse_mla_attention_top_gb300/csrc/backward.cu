@@ -86,6 +86,11 @@ constexpr uint32_t kIdescDqRope = idesc_f32acc(64, 64, 1, 1, kFmtBf16);
 constexpr uint32_t kIdescKv = idesc_f32acc(128, 64, 1, 0, kFmtBf16);
 constexpr uint32_t kIdescKvRope = idesc_f32acc(64, 64, 1, 0, kFmtBf16);
 
+// Programmatic dependent launch: lets the next kernel of the stream begin; waits until the last one has
+// ended and its writes are visible.
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // The part of one row-set that this CTA walks: live tiles j0 .. j1 - 1 (none when j0 >= j1), starting
 // `turn` tiles in and wrapping round. Lists are usually ascending, so that CTAs in step would all
 // add to the same few cache rows at a time; each CTA starts at another place of the list.
@@ -530,6 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const BackwardPar
   tc_fence_after();
   const uint32_t tmem = misc->tmem;
   const WaitCtl wc{p.status, &misc->abort_flag, p.wait_limit_ns ? p.wait_limit_ns : kWaitLimitNs};
+  grid_launch_dependents();
+  grid_wait();  // for prepare_kernel, beside whose end the above ran
   if (warp < kScatWarp0) {
     softmax_role(p, smem, misc, tmem, bars, wc);
   } else if (warp < kFillWarp0) {
@@ -553,6 +560,7 @@ constexpr int kPrepHeads = 32;
 __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const BackwardParams p, const ListParams l,
                                                                int delta_ctas) {
   const int tid = threadIdx.x, lane = tid & 31;
+  grid_launch_dependents();
   if (static_cast<int>(blockIdx.x) < p.T) {
     __shared__ int reach;
     const int t = blockIdx.x;
@@ -635,6 +643,7 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const BackwardPar
 // the cache rows' sums to bf16, eight values at a time.
 constexpr int kJoinRows = 8;
 __global__ void __launch_bounds__(256) finish_kernel(const BackwardParams p, int join_ctas) {
+  grid_wait();
   if (static_cast<int>(blockIdx.x) < join_ctas) {
     const int c = 1 + blockIdx.x / (kRows / kJoinRows), part0 = (blockIdx.x % (kRows / kJoinRows)) * kJoinRows;
     const long long lo = streamk_lo(c, p.total_tiles, p.num_ctas);
@@ -718,13 +727,26 @@ cudaError_t launch_backward(const BackwardParams& p, const ListParams& l, cudaSt
       p, l, delta_ctas);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  backward_kernel<<<static_cast<unsigned>(p.num_ctas), kThreads, kSmem, stream>>>(p);
-  e = cudaGetLastError();
+  // each kernel may begin while the last one ends, and waits for its results (programmatic dependent
+  // launch: the short calls are mostly the kernels' beginnings and ends)
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.num_ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  e = cudaLaunchKernelEx(&cfg, backward_kernel, p);
   if (e != cudaSuccess) return e;
   const int join = (p.num_ctas - 1) * (kRows / kJoinRows);
   const long long n = (p.num_slots * (kRow / 32) + 255) / 256;
-  finish_kernel<<<static_cast<unsigned>(join + (n < 1216 ? n : 1216)), 256, 0, stream>>>(p, join);
-  return cudaGetLastError();
+  cfg.gridDim = dim3(static_cast<unsigned>(join + (n < 1216 ? n : 1216)));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, finish_kernel, p, join);
 }
 
 }  // namespace svt
