@@ -193,6 +193,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
   const bool vec = p.vec != 0;
   const float c = p.inv_tau * kLog2e;
 
+  float mx = -CUDART_INF_F, tmax = -CUDART_INF_F;  // largest candidate (or listed score), largest teacher value
   int held_i[kHeld];
   float held_v[kHeld];
   if constexpr (kFit) {
@@ -203,27 +204,51 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
       held_v[u] = j < p.K ? __ldg(val + j) : 0.f;
     }
   }
-  // f(j, position, value) for the live entries of the list
+  if constexpr (kAll && kFit) mx = fill_part(row, lo, n, vec, part);
+  if constexpr (kFit) {
+    // only the entries this CTA works on: those in its own columns, or every live one of a listed softmax
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const bool live = held_i[u] >= 0 && held_i[u] < len;
+      if (live) tmax = fmaxf(tmax, held_v[u]);
+      if (!live || (kAll && (held_i[u] < lo || held_i[u] >= chi))) held_i[u] = -1;
+    }
+  }
+  float held_x[kHeld];
+  if constexpr (!kAll && kFit) {
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) held_x[u] = held_i[u] >= 0 ? load1(row + held_i[u]) : -CUDART_INF_F;
+  }
+  // f(u, position, value, score) for the entries that this thread works on
   auto entries = [&](auto f) {
     if constexpr (kFit) {
 #pragma unroll
       for (int u = 0; u < kHeld; ++u)
-        if (held_i[u] >= 0 && held_i[u] < len) f(u, held_i[u], held_v[u]);
+        if (held_i[u] >= 0) f(u, held_i[u], held_v[u], held_x[u]);
     } else {
       for (int j = tid; j < p.K; j += kThreads) {
         const int i = __ldg(idx + j);
-        if (i >= 0 && i < len) f(j / kThreads, i, __ldg(val + j));
+        if (i >= 0 && i < len) f(j / kThreads, i, __ldg(val + j), load1(row + i));
       }
     }
   };
+  if (drow != nullptr) {
+    // this CTA's share of the columns behind the candidates
+    const int tail = ((p.N - len + p.split - 1) / p.split + 7) & ~7;
+    const int tlo = min(p.N, len + cr * tail), hi = min(p.N, tlo + tail);
+    int j = tlo;
+    if (vec) {
+      const int al = min(hi, (tlo + 3) & ~3);
+      for (int i = tlo + tid; i < al; i += kThreads) store1(drow + i, 0.f);
+      const int n4 = (hi - al) / 4;
+      for (int i = tid; i < n4; i += kThreads) store4(drow + al + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
+      j = al + 4 * n4;
+    }
+    for (int i = j + tid; i < hi; i += kThreads) store1(drow + i, 0.f);
+  }
 
-  // largest candidate (or listed score) and largest teacher value
-  float mx = -CUDART_INF_F, tmax = -CUDART_INF_F;
-  if constexpr (kAll) {
-    if (kFit) mx = fill_part(row, lo, n, vec, part);
-  } else {
-    if (kFit)
-      for (int j = tid; j < n; j += kThreads) part[j] = 0.f;
+  if constexpr (!kAll && kFit) {
+    for (int j = tid; j < n; j += kThreads) part[j] = 0.f;
   }
   Stats st{-CUDART_INF_F, 0.f, 0.f, 0.f};
   if constexpr (kAll && !kFit) {
@@ -237,10 +262,11 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     }
     mx = st.m;
   }
-  entries([&](int, int i, float v) {
-    if (!kAll) mx = fmaxf(mx, load1(row + i));
-    tmax = fmaxf(tmax, v);
-  });
+  if constexpr (!(kAll && kFit))
+    entries([&](int, int, float v, float x) {
+      if (!kAll) mx = fmaxf(mx, x);
+      tmax = fmaxf(tmax, v);
+    });
   {
     const float4 r = block_reduce<true>(make_float4(mx, tmax, 0.f, 0.f), sh.red[0]);
     st.m = r.x;
@@ -248,18 +274,22 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
   }
   // logits become weights 2^(c (value - max))
   auto weight = [&](float v) { return p.logits ? exp2f((v - tmax) * c) : v; };
-  float base = st.m == -CUDART_INF_F ? 0.f : __fmul_rn(st.m, c);
+  const float base = st.m == -CUDART_INF_F ? 0.f : __fmul_rn(st.m, c);
+  if constexpr (kAll && kFit) {
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) held_x[u] = held_i[u] >= 0 ? part[held_i[u] - lo] : 0.f;
+    __syncthreads();  // every thread has read its listed scores
+  }
+  float held_w[kHeld];
   {
-    // a CTA takes every split-th entry for the sums of the list (each entry of a listed softmax)
     float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
     if (kAll && kFit) r.x = exp_part<true>(part, n, c, base);
-    entries([&](int u, int i, float v) {
-      const bool mine = ((tid + u * kThreads) & (p.split - 1)) == cr;
-      if (kAll && !mine) return;
-      const float x = load1(row + i);
+    entries([&](int u, int, float v, float x) {
       if (!kAll) r.x += exp2f(fmaf(x, c, -base));
-      if (!mine) return;
       const float w = weight(v);
+      if (kFit) held_w[u] = w;
+      // where CTAs see the same entries, each takes every split-th for the sums
+      if (!(kAll && kFit) && ((tid + u * kThreads) & (p.split - 1)) != cr) return;
       r.y += w;
       if (w != 0.f) r.z += w * (p.logits ? (v - x) * c : fmaf(-x, c, log2f(w)));
     });
@@ -267,15 +297,6 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     if (!(kAll && !kFit)) st.s = r.x;
     st.w = r.y;
     st.d = r.z;
-  }
-  // the listed columns of this CTA as they stand, before any of them changes
-  float held_e[kHeld];
-  if constexpr (kAll && kFit) {
-#pragma unroll
-    for (int u = 0; u < kHeld; ++u) {
-      held_e[u] = 0.f;
-      if (held_i[u] >= lo && held_i[u] < chi) held_e[u] = part[held_i[u] - lo];
-    }
   }
 
   float M = st.m, Z = st.s, W = st.w, D = st.d;
@@ -298,25 +319,33 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
         else if (q.s != q.s) Z = q.s;  // NaN scores
       }
     }
-  } else {
-    __syncthreads();  // every thread has read its listed columns
   }
   const float top = M == -CUDART_INF_F ? 0.f : __fmul_rn(M, c);  // Z is relative to it
   // a row without a target, or whose candidates are all -inf, has loss 0 and gradient 0
   const bool some = !(W == 0.f) && !(M == -CUDART_INF_F && !(Z != Z));
   if (p.loss != nullptr && cr == 0 && tid == 0) {
-    // the terms cancel to a small difference: joined in fp64, of which there is one thread's worth (a
-    // logarithm in fp64 would hold the CTA up for microseconds: the fp32 one of the mantissa is as
-    // good next to an exact exponent)
+    // The terms cancel to a small difference: a compensated fp32 sum of D / W with its remainder, the
+    // exact difference of the two bases, and the logarithms of mantissas next to exact exponents (in
+    // fp64, which runs at two lanes a cycle, this took a microsecond that the whole CTA waited for)
     int ez, ew;
     const float mz = frexpf(Z, &ez), mw = frexpf(W, &ew);
-    double inv = static_cast<double>(1.f / W);
-    if (W > 1e-30f && W < 1e30f) inv = inv * (2.0 - W * inv);
-    else inv = 1.0 / W;
-    const double d = static_cast<double>(D) * inv + static_cast<double>(top) -
-                     (p.logits ? static_cast<double>(tmax) * static_cast<double>(c) : 0.0) +
-                     static_cast<double>(ez - ew) + (static_cast<double>(log2f(mz)) - static_cast<double>(log2f(mw)));
-    p.loss[t] = some ? static_cast<float>(d * 0.69314718055994530942) : 0.f;
+    const float quot = __fdiv_rn(D, W), bc = p.logits ? __fmul_rn(tmax, c) : 0.f;
+    float sum = quot, low = 0.f;
+    auto add = [&](float x) {
+      const float u = __fadd_rn(sum, x);
+      low += fabsf(sum) >= fabsf(x) ? __fadd_rn(__fsub_rn(sum, u), x) : __fadd_rn(__fsub_rn(x, u), sum);
+      sum = u;
+    };
+    add(top);
+    add(-bc);
+    if (p.logits) add(-__fmaf_rn(tmax, c, -bc));
+    add(static_cast<float>(ez - ew));
+    add(log2f(mz));
+    add(-log2f(mw));
+    const float rest = __fmaf_rn(-quot, W, D) / W;
+    const float d = sum + (low + rest);
+    // an infinite sum (a weight on a score of -inf) has no remainder
+    p.loss[t] = some ? (fabsf(quot) == CUDART_INF_F ? quot : d) * 0.6931471805599453f : 0.f;
   }
   if (drow == nullptr) return;
 
@@ -326,20 +355,19 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     // part holds 2^(c x - base) of this CTA. A listed column is set to q's share, then p's are added (as
     // often as it is listed); the sweep writes q's share everywhere, and the listed columns again
     const float scale = some ? gq * exp2f(base - top) : 0.f;
-    auto mine = [&](int u) { return held_i[u] >= lo && held_i[u] < chi; };
-#pragma unroll
-    for (int u = 0; u < kHeld; ++u)
-      if (mine(u)) part[held_i[u] - lo] = some ? held_e[u] * scale : 0.f;
-    __syncthreads();
     if (some) {
 #pragma unroll
       for (int u = 0; u < kHeld; ++u)
-        if (mine(u)) atomicAdd(part + (held_i[u] - lo), weight(held_v[u]) * gw);
+        if (held_i[u] >= 0) part[held_i[u] - lo] = ex2_approx(fmaf(held_x[u], c, -base)) * scale;
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u)
+        if (held_i[u] >= 0) atomicAdd(part + (held_i[u] - lo), held_w[u] * gw);
       write_part(part, n, scale, vec, drow + lo);
       __syncthreads();
 #pragma unroll
       for (int u = 0; u < kHeld; ++u)
-        if (mine(u)) store1(drow + held_i[u], part[held_i[u] - lo]);
+        if (held_i[u] >= 0) store1(drow + held_i[u], part[held_i[u] - lo]);
     } else {
       for (int j = tid; j < n; j += kThreads) store1(drow + lo + j, 0.f);
     }
@@ -358,10 +386,10 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
         __syncthreads();
       }
       if (some) {
-        entries([&](int, int i, float v) {
+        entries([&](int, int i, float v, float x) {
           if (i < a || i >= a + m) return;
           float d = weight(v) * gw;
-          if (!kAll) d += exp2f(fmaf(load1(row + i), c, -top)) * gq;
+          if (!kAll) d += exp2f(fmaf(x, c, -top)) * gq;
           if (d != 0.f) atomicAdd(part + (i - a), d);
         });
       }
@@ -369,18 +397,6 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
       write_part(part, m, 1.f, vec, drow + a);
     }
   }
-  // this CTA's share of the columns behind the candidates
-  const int tail = ((p.N - len + p.split - 1) / p.split + 7) & ~7;
-  const int tlo = min(p.N, len + cr * tail), hi = min(p.N, tlo + tail);
-  int j = tlo;
-  if (vec) {
-    const int al = min(hi, (tlo + 3) & ~3);
-    for (int i = tlo + tid; i < al; i += kThreads) store1(drow + i, 0.f);
-    const int n4 = (hi - al) / 4;
-    for (int i = tid; i < n4; i += kThreads) store4(drow + al + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
-    j = al + 4 * n4;
-  }
-  for (int i = j + tid; i < hi; i += kThreads) store1(drow + i, 0.f);
 }
 
 template <typename E, bool kAll>
