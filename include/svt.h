@@ -105,8 +105,8 @@ SVT_API const char* svt_last_error_string(void);
  *                  that announces the first KV tile, so the first wait on it cannot complete.
  *   wait_limit_ns  the time one pipeline wait may take before the kernel gives up, sets
  *                  SVT_DEV_ERR_TIMEOUT and runs to its end (0 = the default, 2 seconds).
- * Applies to the decode and grouped-prefill launches enqueued afterwards by any thread of
- * the process. Returns SVT_ERR_INVALID_ARG for an unknown fault or a negative limit.
+ * Applies to the decode, grouped-prefill and backward launches enqueued afterwards by any thread
+ * of the process. Returns SVT_ERR_INVALID_ARG for an unknown fault or a negative limit.
  */
 SVT_API svt_status svt_debug_pipeline_fault(int32_t fault, int64_t wait_limit_ns);
 
@@ -361,7 +361,7 @@ SVT_API svt_status svt_rope(const void* x, void* out, svt_dtype dtype, int32_t T
  *   freqs         [32] fp64 device array; layout and amplitude as for svt_rope.
  *   q_rope, q_out [T, H, 64] bf16 at element strides (t, h): the queries' rope columns, rotated from
  *                 q_rope into q_out (for instance columns 512 .. 575 of q). Both NULL: no queries.
- * Workspace: the 256-byte status header. One kernel.
+ * Workspace: the 256-byte status header. One kernel. T at most 2^30.
  */
 SVT_API svt_status svt_rope_append(const void* latent_bf16, int64_t latent_stride, const void* k_rope_bf16,
                                    int64_t k_rope_stride, const int32_t* positions, const int32_t* slots, int32_t T,
@@ -387,7 +387,8 @@ SVT_API svt_status svt_rope_append(const void* latent_bf16, int64_t latent_strid
  *   weights       [T, K] fp32 or NULL: each entry's probability summed over the heads (0 for a dead
  *                 entry): what an eviction rule accumulates, or the teacher of svt_distill_topk.
  * P and dS are rounded to bf16 once, as operands of the tensor cores; every sum is fp32. Cache rows'
- * sums are fp32 atomic additions: their order, and so the last bits of dkv, may differ between calls.
+ * sums are fp32 atomic additions: their order, and so the last bits of dkv, may differ between calls
+ * (dq and weights repeat exactly). T * H and K below 2^30, T * K below 2^40. Three kernels.
  * Workspace: svt_sparse_mla_backward_workspace_size(T, H, K, num_pages * page_size); the call leaves
  * its contents behind the status header undefined and needs none of them zero.
  */

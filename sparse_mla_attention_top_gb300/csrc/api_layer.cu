@@ -179,6 +179,7 @@ svt_status svt_rope_append(const void* latent_bf16, int64_t latent_stride, const
   const bool with_q = q_rope_bf16 != nullptr || q_out_bf16 != nullptr;
   st = check_rows(q_rope_bf16, q_out_bf16, 2, T, with_q ? H : 0, kDim, kDim, 0);
   if (st != SVT_OK) return st;
+  if (T > (1 << 30)) return set_last_error(SVT_ERR_UNSUPPORTED, "T must be at most 2^30");
   long long row_stride = 0;
   st = svt::check_kv_cache(kv, &row_stride);
   if (st != SVT_OK) return st;
@@ -258,8 +259,9 @@ svt_status svt_sparse_mla_backward(const void* q_bf16, int32_t T, int32_t H, con
   if (block_table != nullptr && (num_reqs <= 0 || max_blocks <= 0))
     return set_last_error(SVT_ERR_INVALID_ARG, "num_reqs and max_blocks must be > 0 with a block table");
   const long long num_slots = kv->num_pages * static_cast<long long>(kv->page_size);
-  if (static_cast<long long>(T) * H >= (1ll << 30) || static_cast<long long>(T) * K >= (1ll << 40))
-    return set_last_error(SVT_ERR_UNSUPPORTED, "T * H must be below 2^30 and T * K below 2^40");
+  if (static_cast<long long>(T) * H >= (1ll << 30) || static_cast<long long>(T) * K >= (1ll << 40) ||
+      K > (1 << 30))
+    return set_last_error(SVT_ERR_UNSUPPORTED, "T * H and K must be below 2^30 and T * K below 2^40");
   svt::BackwardParams p{};
   p.T = T;
   p.H = H;
@@ -320,11 +322,11 @@ svt_status svt_distill_topk(const void* scores, svt_dtype dtype, int32_t T, int3
     return set_last_error(SVT_ERR_INVALID_ARG, "unknown scope %d", static_cast<int>(scope));
   if (!std::isfinite(temperature) || !(temperature >= 1e-6f) || temperature > 1e6f)
     return set_last_error(SVT_ERR_INVALID_ARG, "temperature must be between 1e-6 and 1e6");
-  if (loss == nullptr && dscores == nullptr)
-    return set_last_error(SVT_ERR_INVALID_ARG, "loss and dscores are both null");
   if (T > 1 && (stride < N || (dscores != nullptr && dstride < N)))
     return set_last_error(SVT_ERR_INVALID_ARG, "row strides must be at least N");
   if (T == 0) return SVT_OK;
+  if (loss == nullptr && dscores == nullptr)
+    return set_last_error(SVT_ERR_INVALID_ARG, "loss and dscores are both null");
   if ((N > 0 && scores == nullptr) || topk == nullptr || teacher == nullptr)
     return set_last_error(SVT_ERR_INVALID_ARG, "scores, topk and teacher must not be null");
   if (!aligned(scores, elem) || !aligned(dscores, elem))

@@ -287,3 +287,85 @@ def test_backward_refuses_an_e4m3_cache(S):
         S.sparse_mla_backward(z(1, 4, 576), kv, z(1, 2, d=torch.int32), SCALE, z(1, 4, 512), z(1, 4, d=torch.float32),
                               z(1, 4, 512), ws=S.Workspace())
     assert e.value.status == S.svt.SVT_ERR_UNSUPPORTED
+
+
+def test_backward_graphs_that_share_a_workspace_replay_in_turn(S):
+    """Two graphs of different sizes captured on one workspace, replayed one after another, the workspace
+    outgrown in between by an eager call."""
+    T, H, K, n = 6, 32, 150, 260
+    ws = S.Workspace()
+    made = []
+    for i, (t, k) in enumerate(((T, K), (2 * T, K // 2))):
+        kv = S.KVCache(normal(70 + i, n, 576).cuda(), n, 1, W.KV_BF16)
+        q, dout, slots = normal(72 + i, t, H, 576).cuda(), normal(74 + i, t, H, 512).cuda(), lists(76 + i, t, k, n).cuda()
+        out, lse = forward(S, q, kv, slots)
+        run = lambda kv=kv, q=q, dout=dout, slots=slots, out=out, lse=lse: S.sparse_mla_backward(  # noqa: E731
+            q, kv, slots, SCALE, out, lse, dout, return_weights=True, ws=ws)
+        want = run()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = run()
+        made.append((g, got, want, (q, kv, slots, out, lse, dout)))
+    big = S.KVCache(normal(80, 5000, 576).cuda(), 5000, 1, W.KV_BF16)
+    q, kv, slots, out, lse, dout = made[0][3]
+    S.sparse_mla_backward(q, big, slots, SCALE, out, lse, dout, ws=ws)
+    junk = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(8)]  # over what was freed, if it was
+    for _ in range(2):
+        for g, got, want, _ in made:
+            for x in got:
+                x.fill_(7)
+            g.replay()
+        torch.cuda.synchronize()
+        for g, got, want, (q, kv, slots, out, lse, dout) in made:
+            assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+            ref, bound = R.backward(q.cpu(), kv.data.cpu(), slots.cpu().long(), SCALE, out.cpu(), lse.cpu(), dout.cpu())
+            R.within(got[1], ref[1], bound[1])
+    del junk
+
+
+def test_backward_and_append_past_32_bit_offsets(S):
+    """A cache of 4.6 GB: rows at both ends, and beyond 2^31 and 2^32 bytes."""
+    n, H, T = 4_000_000, 16, 2
+    cache = torch.zeros((n, 576), dtype=torch.bfloat16, device="cuda")
+    kv = S.KVCache(cache, n // 64, 64, W.KV_BF16)
+    spots = torch.tensor([0, 1, (1 << 31) // 1152 + 1, (1 << 32) // 1152 + 1, n - 2, n - 1], dtype=torch.int32)
+    lat, kr = normal(90, 6, 512), normal(91, 6, 64)
+    f = S.rope_frequencies(64)
+    ws = S.Workspace()
+    pos = torch.arange(6, dtype=torch.int32)
+    S.rope_append(lat.cuda(), kr.cuda(), pos.cuda(), spots.cuda(), kv, f, ws=ws)
+    rows = cache[spots.long().cuda()].cpu()
+    assert torch.equal(rows[:, :512], lat)
+    assert int(torch.count_nonzero(cache[:, 0])) <= 6
+    q, dout = normal(92, T, H, 576).cuda(), normal(93, T, H, 512).cuda()
+    topk = torch.stack([spots, spots.flip(0)]).cuda()
+    out, lse = forward(S, q, kv, topk)
+    dq, dkv, w = S.sparse_mla_backward(q, kv, topk, SCALE, out, lse, dout, return_weights=True, ws=ws)
+    assert ws.read_status() == 0
+    small = torch.arange(6).repeat(T, 1)
+    small[1] = small[1].flip(0)
+    ref, bound = R.backward(q.cpu(), rows, small, SCALE, out.cpu(), lse.cpu(), dout.cpu())
+    for a, b, c in zip((dq, dkv[spots.long().cuda()], w), ref, bound):
+        R.within(a, b, c)
+    dkv[spots.long().cuda()] = 0
+    assert not dkv.any()
+
+
+def test_backward_wait_that_runs_out_is_reported_and_the_next_call_is_clean(S):
+    T, H, K, n = 3, 40, 200, 300
+    kv = S.KVCache(normal(94, n, 576).cuda(), n, 1, W.KV_BF16)
+    q, dout, slots = normal(95, T, H, 576).cuda(), normal(96, T, H, 512).cuda(), lists(97, T, K, n).cuda()
+    out, lse = forward(S, q, kv, slots)
+    ws = S.Workspace()
+    args = (q, kv, slots, SCALE, out, lse, dout)
+    want = S.sparse_mla_backward(*args, return_weights=True, ws=ws)
+    assert ws.read_status() == 0
+    S.debug_pipeline_fault(1, 2_000_000)
+    try:
+        S.sparse_mla_backward(*args, return_weights=True, ws=ws)
+        assert ws.read_status() == S.svt.DEV_ERR_TIMEOUT
+    finally:
+        S.debug_pipeline_fault()
+    got = S.sparse_mla_backward(*args, return_weights=True, ws=ws)
+    assert ws.read_status() == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])

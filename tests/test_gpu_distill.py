@@ -171,3 +171,48 @@ def test_distill_in_a_graph(S):
     g.replay()
     want = S.distill_topk(a, b, c, lens=n)
     assert torch.equal(loss, want[0]) and torch.equal(grad, want[1])
+
+
+def test_distill_empty_sizes(S):
+    for T, N in ((0, 5), (3, 0)):
+        loss, grad = S.distill_topk(torch.zeros((T, N), device="cuda"), torch.zeros((T, 2), dtype=torch.int32, device="cuda"),
+                                    torch.ones((T, 2), device="cuda"))
+        assert loss.shape == (T,) and grad.shape == (T, N) and not loss.any()
+
+
+@pytest.mark.parametrize("scope", ["candidates", "listed"])
+@pytest.mark.parametrize("kind", ["weights", "logits"])
+def test_distill_lists_longer_than_the_registers_hold(S, scope, kind):
+    s, lens, topk, w = case(13, 3, 6000, 5000, torch.float32, kind)
+    check(S, s, lens, topk, w, kind, scope, 1.3)
+
+
+def test_distill_a_small_loss_keeps_its_digits(S):
+    """A student next to its teacher: the loss is a small difference of logarithms. Each entry's difference
+    is rounded to fp32 (values up to 8, differences of a few hundredths), the sums' logarithms to 2^-23."""
+    g = torch.Generator().manual_seed(14)
+    s = torch.randn((64, 900), generator=g) * 2
+    topk = torch.argsort(torch.rand((64, 900), generator=g), 1)[:, :8].sort(1).values.to(torch.int32)
+    v = s.gather(1, topk.long()) + 0.05 * torch.randn((64, 8), generator=g)
+    loss, _ = S.distill_topk(s.cuda(), topk.cuda(), v.cuda(), teacher_kind="logits", over="listed")
+    (ref, _), _ = R.distill(s, None, topk, v, "logits", "listed", 1.0)
+    assert float(ref.max()) < 0.02
+    assert float((loss.double().cpu() - ref).abs().max()) <= 2.0 ** -21
+
+
+def test_distill_on_two_streams_at_once(S):
+    made = [case(15 + i, 40, 20000, 300) for i in range(2)]
+    dev = [[None if t is None else t.cuda() for t in m] for m in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(3):
+        got = []
+        for st, (s, lens, topk, w) in zip(streams, dev):
+            with torch.cuda.stream(st):
+                got.append(S.distill_topk(s, topk, w, lens=lens))
+    torch.cuda.synchronize()
+    for (s, lens, topk, w), (loss, grad) in zip(made, got):
+        (rl, rg), (bl, bg) = R.distill(s, lens, topk, w, "weights", "candidates", 1.0)
+        R.within(loss, rl, bl)
+        R.within(grad, rg, bg + 2.0 ** -24 * rg.abs() + 2.0 ** -126)

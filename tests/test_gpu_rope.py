@@ -217,3 +217,20 @@ def test_rope_append_in_a_graph_and_on_another_stream(S):
     ref = R.rotate(kr.cpu()[:, None], pos.cpu(), f.cpu(), "interleaved")[:, 0]
     got = kv.data.view(torch.bfloat16)[6:11, 512:]
     R.within(got, ref, R.rotate_bound(kr.cpu()[:, None], ref[:, None], "interleaved", torch.bfloat16)[:, 0])
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+def test_rope_negative_large_and_zero_frequencies(S, layout):
+    f = torch.tensor([0.0, -0.75, 1e-12, 3e-320, 41.5, -1e4], dtype=torch.float64)
+    check(S, normal(11, 30, 2, 12, dtype=torch.float32), positions(12, 30), f, layout)
+
+
+def test_rope_broadcast_input_and_refused_overlapping_output(S):
+    f = S.rope_frequencies(64, device="cpu")
+    x = normal(13, 5, 1, 64)
+    wide = x.cuda().expand(5, 7, 64)
+    check(S, x.expand(5, 7, 64), positions(14, 5), f, "half", x_dev=wide)
+    with pytest.raises(S.SvtError):
+        S.rope(wide, positions(14, 5).cuda(), f.cuda(), out=wide)
+    with pytest.raises(TypeError):
+        S.rope(wide, positions(14, 5), f.cuda())  # positions on the CPU

@@ -113,6 +113,7 @@ def test_rope_append_refusals(L):
     bad, uns = svt.SVT_ERR_INVALID_ARG, svt.SVT_ERR_UNSUPPORTED
     assert call(lat=None) == bad and call(kr=None) == bad and call(pos=None) == bad and call(slots=None) == bad
     assert call(lat=ctypes.c_void_p(0x10008)) == bad and call(ls=516) == bad and "16-byte" in err(L)
+    assert call(T=(1 << 30) + 1) == uns
     assert call(T=-1) == bad and call(fr=None) == bad and call(layout=5) == bad and call(amp=float("inf")) == bad
     assert call(kv=_kv(dtype=3)) == uns and call(kv=_kv(pages=0)) == bad and call(kv=_kv(stride=100)) == bad
     assert call(ws=None) == bad and call(n=128) == svt.SVT_ERR_WORKSPACE
@@ -136,7 +137,7 @@ def test_backward_refusals(L):
     assert call(kv=_kv(dtype=1)) == uns and "bf16" in err(L)
     assert call(kv=_kv(pages=1 << 26)) == uns and call(kv=_kv(data=0x10008)) == bad
     assert call(bt=A) == bad
-    assert call(T=1 << 26, K=1 << 20) == uns
+    assert call(T=1 << 26, K=1 << 20) == uns and call(K=(1 << 30) + 1) == uns and call(T=1 << 24) == uns
     for name in ("q", "out", "dout", "dq", "dkv"):
         assert call(**{name: None}) == bad and call(**{name: odd}) == bad, name
     assert call(lse=None) == bad and call(topk=None) == bad
@@ -174,3 +175,19 @@ def test_bindings_refuse_tensors_the_kernels_cannot_take(L):
                  lambda: S.distill_topk(x[0].float().t(), pos[None], x[0].float())):
         with pytest.raises(TypeError):
             call()
+
+
+def test_frequencies_on_a_negative_or_fractional_base(L):
+    assert torch.allclose(freqs(4, base=0.25), torch.tensor([1.0, 2.0], dtype=torch.float64), rtol=1e-15, atol=0)
+    with pytest.raises(S.SvtError):
+        freqs(4, base=-2.0)
+
+
+def test_the_binding_refuses_what_is_no_tensor(L):
+    for args in ((None,) * 8, (1, 2, 3, 0, 0, False, 1.0, None)):
+        with pytest.raises(TypeError):
+            svt._binding().rope(*args)
+    with pytest.raises(TypeError):
+        svt._binding().rope(torch.zeros(1, 1, 2))
+    with pytest.raises(ValueError):
+        S.rope(torch.zeros(1, 1, 2), torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.float64), layout="x")
