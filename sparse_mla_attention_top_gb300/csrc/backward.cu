@@ -296,37 +296,51 @@ __device__ __forceinline__ void add_rows(float* dst, const int* slots, const uin
   const int lane = threadIdx.x & 31;
   constexpr int kLow = kRope ? 4 : 8;      // lanes that hold one entry afterwards
   constexpr int kStep = kRope ? 8 : 4;     // entries per instruction
+  constexpr int kBatch = 16 / kStep;       // instructions prepared together
   const bool up = (lane & kLow) != 0, top = (lane & (2 * kLow)) != 0;
   dst += (lane & (kLow - 1)) * 4;
 #pragma unroll
-  for (int i = 0; i < 32; i += kStep) {
-    uint32_t x[4] = {v[i], v[i + 1], v[i + 2], v[i + 3]};
-    if constexpr (kRope) {
-      // the upper lanes hold nothing: they take entries i + 4 .. i + 7
+  for (int i0 = 0; i0 < 32; i0 += kBatch * kStep) {
+    uint32_t x[kBatch][4];
+    int slot[kBatch];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const uint32_t o = __shfl_sync(0xffffffffu, v[i + 4 + u], lane & 15);
-        if (lane >= 16) x[u] = o;
+    for (int n = 0; n < kBatch; ++n) {
+      const int i = i0 + n * kStep;
+      slot[n] = slots[i + (lane / kLow)];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) x[n][u] = v[i + u];
+      if constexpr (kRope) {
+        // the upper lanes hold nothing: they take entries i + 4 .. i + 7
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t o = __shfl_sync(0xffffffffu, v[i + 4 + u], lane & 15);
+          if (lane >= 16) x[n][u] = o;
+        }
       }
     }
 #pragma unroll
-    for (int u = 0; u < 4; u += 2) {
-      const uint32_t o = __shfl_xor_sync(0xffffffffu, up ? x[u] : x[u + 1], kLow);
-      if (up) x[u] = o;
-      else x[u + 1] = o;
-    }
+    for (int n = 0; n < kBatch; ++n)
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint32_t o = __shfl_xor_sync(0xffffffffu, top ? x[u] : x[u + 2], 2 * kLow);
-      if (top) x[u] = o;
-      else x[u + 2] = o;
-    }
-    const int slot = slots[i + (lane / kLow)];
-    if (slot >= 0)
-      asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst + static_cast<long long>(slot) * kRow),
-                   "f"(__uint_as_float(x[0])), "f"(__uint_as_float(x[1])), "f"(__uint_as_float(x[2])),
-                   "f"(__uint_as_float(x[3]))
-                   : "memory");
+      for (int u = 0; u < 4; u += 2) {
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, up ? x[n][u] : x[n][u + 1], kLow);
+        if (up) x[n][u] = o;
+        else x[n][u + 1] = o;
+      }
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, top ? x[n][u] : x[n][u + 2], 2 * kLow);
+        if (top) x[n][u] = o;
+        else x[n][u + 2] = o;
+      }
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n)
+      if (slot[n] >= 0)
+        asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst + static_cast<long long>(slot[n]) * kRow),
+                     "f"(__uint_as_float(x[n][0])), "f"(__uint_as_float(x[n][1])), "f"(__uint_as_float(x[n][2])),
+                     "f"(__uint_as_float(x[n][3]))
+                     : "memory");
   }
 }
 
