@@ -5,8 +5,7 @@
 // and a cache row's gradient is the sum of dK (+ dV on the latent columns) over the lists that
 // hold it. sum over heads of P is each entry's attention weight.
 //
-// Three kernels. prepare resolves the lists, forms delta and lse in log2 units and zeroes the cache
-// rows' sums. The main kernel walks (row-set, 64-entry tile) pairs, a row-set being up to 64 heads of
+// Three kernels. prepare resolves the lists, forms delta and zeroes the cache rows' sums. The main kernel walks (row-set, 64-entry tile) pairs, a row-set being up to 64 heads of
 // one query, one persistent CTA per SM with an equal share of all tiles (stream-K). finish joins the
 // dq of row-sets cut between CTAs (fp32, in a fixed order) and rounds the cache rows' sums to bf16.
 //
@@ -353,7 +352,6 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
   // their heads 32 half + 8 k + 2 (lane & 3) and the next, k < 4
   const int e = 16 * quad + (lane >> 2), pair = lane & 3;
   const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
-  const float scale_log2 = p.scale * kLog2e;
   // where this lane's row of the stored 8 x 8 matrices goes: matrix lane >> 3 is chunk 4 half + that
   const uint32_t at0 = smem_u32(smem) + sw128_offset(16 * quad + (lane & 7), 4 * half + (lane >> 3));
   const uint32_t at8 = at0 + 8 * 128;
@@ -365,12 +363,14 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
   Seg s;
   while (it.next(s)) {
     const bool any = s.j0 < s.j1;
-    float lse2[8], delta[8];  // delta times the softmax scale
+    // the exponent S - lse is one fma and takes its factor log2 e afterwards: lse in log2 units would be
+    // off by 2^-24 of itself, here the rounding is relative to the difference
+    float lse[8], delta[8];  // delta times the softmax scale
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = 32 * half + 8 * (i >> 1) + 2 * pair + (i & 1);
       const float2 v = r < s.nvalid ? p.stats[s.base + r] : make_float2(CUDART_INF_F, 0.f);
-      lse2[i] = v.x;
+      lse[i] = v.x;
       delta[i] = v.y * p.scale;
     }
     // the second half leaves its sums in shared memory; the first adds them once the tile's first block of
@@ -406,7 +406,7 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
           for (int u = 0; u < 2; ++u) {
             const int i = 4 * k + 2 * h + u;
             // a dead entry's row is zero: with P = 0, its dS is 0 too
-            const float x = ex2_approx(fmaf(__uint_as_float(sv[i]), scale_log2, -lse2[2 * k + u]));
+            const float x = ex2_approx(fmaf(__uint_as_float(sv[i]), p.scale, -lse[2 * k + u]) * kLog2e);
             pr[u] = (h ? live8 : live0) ? x : 0.f;
             d[u] = pr[u] * fmaf(__uint_as_float(dv[i]), p.scale, -delta[2 * k + u]);
             if (h) w8 += pr[u];
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const BackwardPar
 }
 
 // CTAs 0 .. T - 1: a query's list as cache rows, and how far the live ones reach. The next delta_ctas,
-// 32 heads of any queries each: (lse in log2 units, delta); a head without a live entry (lse = -inf)
+// 32 heads of any queries each: (lse, delta); a head without a live entry (lse = -inf)
 // gets +inf, so that P = 0. The others zero the cache rows' sums.
 constexpr int kPrepThreads = 256;
 constexpr int kPrepHeads = 32;
@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const BackwardPar
       for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
       if (lane == 0) {
         const float lse = p.lse[r];
-        p.stats[r] = make_float2(lse == -CUDART_INF_F ? CUDART_INF_F : lse * kLog2e, d - (p.dlse ? p.dlse[r] : 0.f));
+        p.stats[r] = make_float2(lse == -CUDART_INF_F ? CUDART_INF_F : lse, d - (p.dlse ? p.dlse[r] : 0.f));
       }
     }
   }
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const BackwardPar
 // CTAs below join_ctas join the dq of the row-set that the border before CTA c + 1 of the main
 // kernel cuts (the first such border of the row-set does it), 8 rows each; the others round
 // the cache rows' sums to bf16, eight values at a time.
-constexpr int kJoinRows = 8;
+constexpr int kJoinRows = 4;
 __global__ void __launch_bounds__(256) finish_kernel(const BackwardParams p, int join_ctas) {
   grid_wait();
   if (static_cast<int>(blockIdx.x) < join_ctas) {

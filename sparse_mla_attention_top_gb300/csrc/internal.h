@@ -264,7 +264,7 @@ struct BackwardParams {
   // scratch
   int32_t* slots;     // [T, K] resolved, -1 = dead
   int32_t* live_len;  // [T] entries up to the last live one
-  float2* stats;      // [T, H]: lse in log2 units (+inf for a head with no live entry), delta
+  float2* stats;      // [T, H]: lse (+inf for a head with no live entry), delta
   float* dq_part;     // [2 * num_ctas, 64, 576]: dq of row-sets cut between CTAs
   float* dkv_acc;     // [num_slots, 576]
   int* status;
