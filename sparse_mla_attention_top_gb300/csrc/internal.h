@@ -203,7 +203,7 @@ struct RopeParams {
   const int32_t* positions;  // [T]
   const double* freqs;       // [dim / 2] radians per position
   float amplitude, sign;     // sign: 1, or -1 for the transposed rotation
-  int units, rot_units, rows_per_cta;
+  int units, rot_units, copy_cols, rows_per_cta;
   uint32_t magic_units, magic_h;
 };
 cudaError_t launch_rope(const RopeParams& p, bool f32, bool half, cudaStream_t stream);

@@ -11,11 +11,11 @@
 // product would be off by 0.06 rad at position 10^6. The table of a CTA's tokens is computed
 // once in shared memory and used by all of their heads.
 //
-// Bound: reading and writing the columns. A thread takes one 16-byte unit at a time, the first loaded
-// before the angles are known, and full occupancy keeps the loads in flight (four units a thread at
-// 64 registers: 72 instead of 74 us on 8192 tokens x 64 heads x 192 columns, but 14.4 instead of 12.5 us
-// on 8192 cache rows with 16 heads; a copy of the first one's bytes takes 63 us); rows that do not start on 16-byte boundaries (or dims that do
-// not split into 16-byte units) take the same kernel on single pairs.
+// Bound: reading and writing the columns, and next to that the instructions that find them: a thread
+// takes two units, of one or two 16-byte pieces each, loaded before the angles are known; six CTAs of
+// 256 threads share an SM. 8192 tokens x 64 heads x 192 columns (64 rotated): 63.6 us, 6.3 TB/s, as
+// long as a plain copy of them (one piece a unit: 74 us). Rows that do not start on 16-byte
+// boundaries (or dims that do not split into 16-byte pieces) take the same kernel on single pairs.
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -29,9 +29,9 @@ namespace svt {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeUnroll = 1;   // units a thread loads at once
-constexpr int kRopeCtas = 8;     // resident CTAs per SM (32 registers a thread)
-constexpr int kRopeBatches = 2;  // batches of a full CTA
+constexpr int kRopeUnroll = 2;   // units a thread loads at once
+constexpr int kRopeCtas = 6;     // resident CTAs per SM (40 registers a thread)
+constexpr int kRopeBatches = 1;  // batches of a full CTA
 
 // The angle of position `pos` at `freq` radians per position, in half turns in [-1, 1). The fraction
 // of a turn, freq / 2 pi modulo 1 in units of 2^-64, comes from the double's 53-bit mantissa times
@@ -135,7 +135,7 @@ __device__ __forceinline__ void rope_rows(const RopeParams& p, long long blk, fl
         if (un < p.rot_units) {
           col = p.offset + un * (kVec || kHalf ? kE : 2);
         } else {
-          col = (un - p.rot_units) * kE;
+          col = (un - p.rot_units) * p.copy_cols;
           if (col >= p.offset) col += p.dim;
         }
         const E* src = x + (t0 + t) * p.x_stride_t + h * p.x_stride_h + col;
@@ -146,6 +146,8 @@ __device__ __forceinline__ void rope_rows(const RopeParams& p, long long blk, fl
         if (un < p.rot_units) {
           if (kHalf) q.b[u] = *reinterpret_cast<const Reg*>(src + pairs);
           else if (!kVec) q.b[u] = *reinterpret_cast<const Reg*>(src + 1);
+        } else if (p.copy_cols > kE) {
+          q.b[u] = *reinterpret_cast<const Reg*>(src + kE);
         }
       }
     }
@@ -157,6 +159,7 @@ __device__ __forceinline__ void rope_rows(const RopeParams& p, long long blk, fl
       E* dst = out + q.dst[u];
       if (q.unit[u] >= p.rot_units) {
         *reinterpret_cast<Reg*>(dst) = q.a[u];
+        if (p.copy_cols > kE) *reinterpret_cast<Reg*>(dst + kE) = q.b[u];
         continue;
       }
       const float2* cs = table + q.tl[u] * pairs;
@@ -320,9 +323,11 @@ long long plan_rope(RopeParams& p, int elem, bool half, int sms, bool* vec) {
          al(half ? p.dim / 2 : p.dim);
   const bool copy = p.x != p.out;
   p.rot_units = *vec ? (half ? p.dim / 2 : p.dim) / e : p.dim / 2;
-  p.units = p.rot_units + (copy ? (p.D - p.dim) / (*vec ? e : 1) : 0);
+  // copied columns go two 16-byte pieces a unit where both sides of the rotated ones allow it
+  p.copy_cols = *vec ? (p.offset % (2 * e) == 0 && (p.D - p.dim - p.offset) % (2 * e) == 0 ? 2 * e : e) : 1;
+  p.units = p.rot_units + (copy ? (p.D - p.dim) / p.copy_cols : 0);
   const long long total = static_cast<long long>(p.T) * p.H;
-  // a full CTA takes two batches; when that leaves SMs idle, fewer rows
+  // a full CTA takes one batch; when that leaves SMs idle, fewer rows
   long long rows = kRopeThreads * kRopeUnroll * kRopeBatches / p.units;
   const long long fill = (total + 2ll * sms - 1) / (2ll * sms);
   if (rows > fill) rows = fill;
