@@ -17,7 +17,6 @@
 // put right behind it. A list of up to 2048 entries stays in registers, and the CTAs of a row share
 // out its sums. Three CTAs of 512 threads share an SM, so one's reads overlap another's writes.
 // Longer lists, and rows of more than eight parts, are read again where they are needed.
-#include <cooperative_groups.h>
 #include <math_constants.h>
 
 #include <cstdint>
@@ -41,9 +40,11 @@ struct Stats {
 };
 
 struct DistillShared {
-  float4 red[2][kWarps];   // one array per reduction, in turns
-  Stats stats[kMaxSplit];  // every CTA's, pushed by each
+  float4 red[2][kWarps];               // one array per reduction, in turns
+  alignas(16) Stats stats[kMaxSplit];  // every CTA's, sent by each
+  uint64_t arrived;                    // counts their bytes
 };
+static_assert(sizeof(Stats) == 16, "one message");
 
 // Three sums over the block (x, y, z), or with kMax two maxima (x, y; NaN ignored). One barrier; `red`
 // alternates between calls, so that a slow warp still reads the previous array.
@@ -175,9 +176,15 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
   extern __shared__ float4 dyn[];
   float* part = reinterpret_cast<float*>(dyn);
   __shared__ DistillShared sh;
-  auto cl = cooperative_groups::this_cluster();
-  // (completed below) every CTA of the cluster has started
-  if (p.split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  if (p.split > 1) {
+    if (threadIdx.x == 0) {
+      mbar_init(smem_u32(&sh.arrived), 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      mbar_arrive_expect_tx(smem_u32(&sh.arrived), p.split * static_cast<uint32_t>(sizeof(Stats)));
+    }
+    // (completed below) every CTA of the cluster has started and can be sent to
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  }
   const int tid = threadIdx.x;
   const int t = blockIdx.x / p.split, cr = blockIdx.x - t * p.split;
   const E* row = static_cast<const E*>(p.scores) + static_cast<long long>(t) * p.stride;
@@ -300,10 +307,22 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
   }
 
   float M = st.m, Z = st.s, W = st.w, D = st.d;
+  bool lost = false;
   if (p.split > 1) {
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    if (tid < p.split) cl.map_shared_rank(&sh, static_cast<unsigned>(tid))->stats[cr] = st;
-    cl.sync();  // every CTA's statistics are here
+    if (tid < p.split)
+      st_async_v4(mapa_shared(smem_u32(&sh.stats[cr]), tid),
+                  make_uint4(__float_as_uint(st.m), __float_as_uint(st.s), __float_as_uint(st.w), __float_as_uint(st.d)),
+                  mapa_shared(smem_u32(&sh.arrived), tid));
+    // every CTA's sums arrive here (a barrier of the cluster would also wait for the zeroes on their way
+    // to memory); should one not, the row's loss and gradient are NaN
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait_cluster(smem_u32(&sh.arrived), 0)) {
+      if (globaltimer() - t0 > kWaitLimitNs) {
+        lost = true;
+        break;
+      }
+    }
     W = D = 0.f;
     for (int r = 0; r < p.split; ++r) {
       W += sh.stats[r].w;
@@ -320,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
       }
     }
   }
+  if (lost) Z = W = __uint_as_float(0x7FC00000u);
   const float top = M == -CUDART_INF_F ? 0.f : __fmul_rn(M, c);  // Z is relative to it
   // a row without a target, or whose candidates are all -inf, has loss 0 and gradient 0
   const bool some = !(W == 0.f) && !(M == -CUDART_INF_F && !(Z != Z));
