@@ -1,4 +1,4 @@
-"""Thin Python binding of libsvt.so (ctypes).
+"""Thin Python binding of libsvt.so (ctypes, and csrc/binding.cpp for the short calls).
 
 Argument marshalling only: every function takes torch tensors on the current CUDA device,
 checks dtypes and shapes, passes raw pointers and the current stream to the C ABI, and
