@@ -389,8 +389,9 @@ SVT_API svt_status svt_rope_append(const void* latent_bf16, int64_t latent_strid
  * P and dS are rounded to bf16 once, as operands of the tensor cores; every sum is fp32. Cache rows'
  * sums are fp32 atomic additions: their order, and so the last bits of dkv, may differ between calls
  * (dq and weights repeat exactly). T * H and K below 2^30, T * K below 2^40. Three kernels.
- * Workspace: svt_sparse_mla_backward_workspace_size(T, H, K, num_pages * page_size); the call leaves
- * its contents behind the status header undefined and needs none of them zero.
+ * Workspace: svt_sparse_mla_backward_workspace_size(T, H, K, num_pages * page_size), which depends on
+ * the current device's SM count; the call leaves its contents behind the status header undefined and
+ * needs none of them zero.
  */
 SVT_API size_t svt_sparse_mla_backward_workspace_size(int32_t T, int32_t H, int32_t K, int64_t num_slots);
 SVT_API svt_status svt_sparse_mla_backward(const void* q_bf16, int32_t T, int32_t H, const svt_kv_cache* kv,
@@ -420,7 +421,7 @@ SVT_API svt_status svt_sparse_mla_backward(const void* q_bf16, int32_t T, int32_
  *                 overlap scores; all N columns are written.
  * A query whose teacher values are all 0 (or which has no live entry), or whose scores are all -inf,
  * has loss 0 and gradient 0. A listed score of -inf among others gives an infinite loss; NaN inputs
- * give NaN in their own row alone. One kernel, no workspace.
+ * give NaN in their own row alone. N and K at most 2^30, T at most 2^27. One kernel, no workspace.
  */
 typedef enum { SVT_TEACHER_WEIGHTS = 0, SVT_TEACHER_LOGITS = 1 } svt_teacher_kind;
 typedef enum { SVT_DISTILL_CANDIDATES = 0, SVT_DISTILL_LISTED = 1 } svt_distill_scope;

@@ -315,7 +315,8 @@ svt_status svt_distill_topk(const void* scores, svt_dtype dtype, int32_t T, int3
   const int elem = dtype == SVT_F32 ? 4 : 2;
   if (T < 0 || N < 0) return set_last_error(SVT_ERR_INVALID_ARG, "T and N must be >= 0");
   if (K < 1) return set_last_error(SVT_ERR_INVALID_ARG, "K must be >= 1");
-  if (N > (1 << 30) || T > (1 << 27)) return set_last_error(SVT_ERR_UNSUPPORTED, "N is limited to 2^30, T to 2^27");
+  if (N > (1 << 30) || K > (1 << 30) || T > (1 << 27))
+    return set_last_error(SVT_ERR_UNSUPPORTED, "N and K are limited to 2^30, T to 2^27");
   if (kind != SVT_TEACHER_WEIGHTS && kind != SVT_TEACHER_LOGITS)
     return set_last_error(SVT_ERR_INVALID_ARG, "unknown teacher kind %d", static_cast<int>(kind));
   if (scope != SVT_DISTILL_CANDIDATES && scope != SVT_DISTILL_LISTED)

@@ -3,12 +3,14 @@
 //   p = the list's values normalised (weights), or softmax(value / tau) (logits),
 //   q = softmax(x / tau) over all candidates, or over the listed ones,
 //   loss = sum_j p_j (ln p_j - ln q_j),   d loss / d x_n = (q_n - sum of p at n) / tau.
-// Everything runs in log2 units (c = log2(e) / tau), exponents relative to the row's largest score. With
-// weights w, W = sum w, and the student's normaliser L = log2 sum 2^(c x):
-//   weights: loss = sum w (log2 w - c x) / W - log2 W + L,
-//   logits:  loss = sum w (c value - c x) / W - c max - log2 W + L,  w = 2^(c (value - max)),
-// so one sweep over the list serves the loss; an entry's two logarithms are subtracted before they
-// are summed, which keeps a small loss of long logarithms.
+// Everything runs in log2 units (c = log2(e) / tau) and relative to the largest score m and the largest
+// teacher value v_m. With w = 2^(c (v - v_m)) (logits) or v / v_m (weights), W = sum w and
+// Z = sum 2^(c (x - m)):
+//   loss = sum w e / W - log2 W + log2 Z,
+//   e = c ((v - x) - (v_m - m)) (logits) or log2 w - c (x - m) (weights),
+// so one sweep over the list serves the loss. An entry's two logarithms are subtracted before they are
+// summed, which keeps the digits of a small loss of long logarithms, and a list of one entry has
+// exactly no loss and no gradient.
 //
 // Bound: reading the scores once and writing the gradient once. A row is cut between the CTAs
 // of a cluster so that each part (up to 64 KB) stays in shared memory: it is read from memory
@@ -128,24 +130,24 @@ __device__ __forceinline__ float fill_part(const E* row, int a, int n, bool vec,
   return mx;
 }
 
-// This thread's sum of 2^(c x - base) over part[0 .. n), which are left in place of x with kKeep.
-// The exponent is one fma: its error is relative to c (x - max), small where the terms are large.
+// This thread's sum of 2^(c (x - ref)) over part[0 .. n), which are left in place of x with kKeep. The
+// difference comes first: its rounding is relative to x - ref, small where the terms are large.
 template <bool kKeep>
-__device__ __forceinline__ float exp_part(float* part, int n, float c, float base) {
+__device__ __forceinline__ float exp_part(float* part, int n, float c, float ref) {
   float s = 0.f;
   const int n4 = n / 4;
 #pragma unroll 4
   for (int j = threadIdx.x; j < n4; j += kThreads) {
     float4 v = reinterpret_cast<float4*>(part)[j];
-    v.x = ex2_approx(fmaf(v.x, c, -base));
-    v.y = ex2_approx(fmaf(v.y, c, -base));
-    v.z = ex2_approx(fmaf(v.z, c, -base));
-    v.w = ex2_approx(fmaf(v.w, c, -base));
+    v.x = ex2_approx((v.x - ref) * c);
+    v.y = ex2_approx((v.y - ref) * c);
+    v.z = ex2_approx((v.z - ref) * c);
+    v.w = ex2_approx((v.w - ref) * c);
     s += (v.x + v.y) + (v.z + v.w);
     if (kKeep) reinterpret_cast<float4*>(part)[j] = v;
   }
   for (int j = 4 * n4 + threadIdx.x; j < n; j += kThreads) {
-    const float v = ex2_approx(fmaf(part[j], c, -base));
+    const float v = ex2_approx((part[j] - ref) * c);
     s += v;
     if (kKeep) part[j] = v;
   }
@@ -264,8 +266,8 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
       const int m = min(kPart, chi - a);
       const float nm = fmaxf(st.m, block_reduce<true>(make_float4(fill_part(row, a, m, vec, part), 0.f, 0.f, 0.f), sh.red[0]).x);
       const float s = block_reduce<false>(
-          make_float4(exp_part<false>(part, m, c, nm == -CUDART_INF_F ? 0.f : __fmul_rn(nm, c)), 0.f, 0.f, 0.f), sh.red[1]).x;
-      st.s = (st.m == -CUDART_INF_F ? 0.f : st.s * exp2f(__fmul_rn(st.m, c) - __fmul_rn(nm, c))) + s;
+          make_float4(exp_part<false>(part, m, c, nm == -CUDART_INF_F ? 0.f : nm), 0.f, 0.f, 0.f), sh.red[1]).x;
+      st.s = (st.m == -CUDART_INF_F ? 0.f : st.s * exp2f((st.m - nm) * c)) + s;
       st.m = nm;
     }
     mx = st.m;
@@ -280,9 +282,8 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     st.m = r.x;
     tmax = r.y == -CUDART_INF_F ? 0.f : r.y;  // nothing listed: every weight is 0
   }
-  // logits become weights 2^(c (value - max))
-  auto weight = [&](float v) { return p.logits ? exp2f((v - tmax) * c) : v; };
-  const float base = st.m == -CUDART_INF_F ? 0.f : __fmul_rn(st.m, c);
+  auto weight = [&](float v) { return p.logits ? exp2f((v - tmax) * c) : (tmax > 0.f ? v / tmax : v); };
+  const float ref = st.m == -CUDART_INF_F ? 0.f : st.m;  // of this CTA's exponents
   if constexpr (kAll && kFit) {
 #pragma unroll
     for (int u = 0; u < kHeld; ++u) held_x[u] = held_i[u] >= 0 ? part[held_i[u] - lo] : 0.f;
@@ -291,15 +292,15 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
   float held_w[kHeld];
   {
     float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (kAll && kFit) r.x = exp_part<true>(part, n, c, base);
+    if (kAll && kFit) r.x = exp_part<true>(part, n, c, ref);
     entries([&](int u, int, float v, float x) {
-      if (!kAll) r.x += exp2f(fmaf(x, c, -base));
+      if (!kAll) r.x += exp2f((x - ref) * c);
       const float w = weight(v);
       if (kFit) held_w[u] = w;
       // where CTAs see the same entries, each takes every split-th for the sums
       if (!(kAll && kFit) && ((tid + u * kThreads) & (p.split - 1)) != cr) return;
       r.y += w;
-      if (w != 0.f) r.z += w * (p.logits ? (v - x) * c : fmaf(-x, c, log2f(w)));
+      if (w != 0.f) r.z += w * (p.logits ? ((v - x) - (tmax - ref)) * c : fmaf(ref - x, c, log2f(w)));
     });
     r = block_reduce<false>(r, sh.red[1]);
     if (!(kAll && !kFit)) st.s = r.x;
@@ -324,42 +325,43 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
         break;
       }
     }
-    W = D = 0.f;
-    for (int r = 0; r < p.split; ++r) {
-      W += sh.stats[r].w;
-      D += sh.stats[r].d;
-    }
     if constexpr (kAll) {
       M = -CUDART_INF_F;
       for (int r = 0; r < p.split; ++r) M = fmaxf(M, sh.stats[r].m);
       Z = 0.f;
-      for (int r = 0; r < p.split; ++r) {
-        const Stats q = sh.stats[r];
-        if (q.m != -CUDART_INF_F) Z += q.s * exp2f(__fmul_rn(q.m, c) - __fmul_rn(M, c));
+    }
+    W = D = 0.f;
+    for (int r = 0; r < p.split; ++r) {
+      const Stats q = sh.stats[r];
+      // its exponents and its e's were relative to its own largest score
+      const float up = kAll && M != -CUDART_INF_F ? (q.m == -CUDART_INF_F ? 0.f : q.m) - M : 0.f;
+      if (q.w != 0.f) {
+        W += q.w;
+        D += q.d - q.w * (up * c);
+      }
+      if constexpr (kAll) {
+        if (q.m != -CUDART_INF_F) Z += q.s * exp2f(up * c);
         else if (q.s != q.s) Z = q.s;  // NaN scores
       }
     }
   }
   if (lost) Z = W = __uint_as_float(0x7FC00000u);
-  const float top = M == -CUDART_INF_F ? 0.f : __fmul_rn(M, c);  // Z is relative to it
+  const float top = M == -CUDART_INF_F ? 0.f : M;  // Z is relative to it
   // a row without a target, or whose candidates are all -inf, has loss 0 and gradient 0
   const bool some = !(W == 0.f) && !(M == -CUDART_INF_F && !(Z != Z));
   if (p.loss != nullptr && cr == 0 && tid == 0) {
-    // The terms cancel to a small difference: a compensated fp32 sum of D / W with its remainder, the
-    // exact difference of the two bases, and the logarithms of mantissas next to exact exponents (in
-    // fp64, which runs at two lanes a cycle, this took a microsecond that the whole CTA waited for)
+    // The terms may cancel to a small difference: a compensated fp32 sum of D / W, the logarithms of
+    // mantissas next to exact exponents, and the division's remainder (in fp64, which runs at two lanes a
+    // cycle, this took a microsecond that the whole CTA waited for)
     int ez, ew;
     const float mz = frexpf(Z, &ez), mw = frexpf(W, &ew);
-    const float quot = __fdiv_rn(D, W), bc = p.logits ? __fmul_rn(tmax, c) : 0.f;
+    const float quot = __fdiv_rn(D, W);
     float sum = quot, low = 0.f;
     auto add = [&](float x) {
       const float u = __fadd_rn(sum, x);
       low += fabsf(sum) >= fabsf(x) ? __fadd_rn(__fsub_rn(sum, u), x) : __fadd_rn(__fsub_rn(x, u), sum);
       sum = u;
     };
-    add(top);
-    add(-bc);
-    if (p.logits) add(-__fmaf_rn(tmax, c, -bc));
     add(static_cast<float>(ez - ew));
     add(log2f(mz));
     add(-log2f(mw));
@@ -373,13 +375,13 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
   const float g = some ? (p.row_weight ? p.row_weight[t] : 1.f) * p.inv_tau : 0.f;
   const float gq = some ? g / Z : 0.f, gw = some ? -g / W : 0.f;
   if constexpr (kAll && kFit) {
-    // part holds 2^(c x - base) of this CTA. A listed column is set to q's share, then p's are added (as
+    // part holds 2^(c (x - ref)). A listed column is set to q's share, then p's are added (as
     // often as it is listed); the sweep writes q's share everywhere, and the listed columns again
-    const float scale = some ? gq * exp2f(base - top) : 0.f;
+    const float scale = some ? gq * exp2f((ref - top) * c) : 0.f;
     if (some) {
 #pragma unroll
       for (int u = 0; u < kHeld; ++u)
-        if (held_i[u] >= 0) part[held_i[u] - lo] = ex2_approx(fmaf(held_x[u], c, -base)) * scale;
+        if (held_i[u] >= 0) part[held_i[u] - lo] = ex2_approx((held_x[u] - ref) * c) * scale;
       __syncthreads();
 #pragma unroll
       for (int u = 0; u < kHeld; ++u)
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
         __syncthreads();
         fill_part(row, a, m, vec, part);
         __syncthreads();
-        for (int j = tid; j < m; j += kThreads) part[j] = some ? ex2_approx(fmaf(part[j], c, -top)) * gq : 0.f;
+        for (int j = tid; j < m; j += kThreads) part[j] = some ? ex2_approx((part[j] - top) * c) * gq : 0.f;
         __syncthreads();
       } else if constexpr (!kFit) {
         __syncthreads();
@@ -410,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
         entries([&](int, int i, float v, float x) {
           if (i < a || i >= a + m) return;
           float d = weight(v) * gw;
-          if (!kAll) d += exp2f(fmaf(x, c, -top)) * gq;
+          if (!kAll) d += exp2f((x - top) * c) * gq;
           if (d != 0.f) atomicAdd(part + (i - a), d);
         });
       }

@@ -216,3 +216,32 @@ def test_distill_on_two_streams_at_once(S):
         (rl, rg), (bl, bg) = R.distill(s, lens, topk, w, "weights", "candidates", 1.0)
         R.within(loss, rl, bl)
         R.within(grad, rg, bg + 2.0 ** -24 * rg.abs() + 2.0 ** -126)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["weights", "logits"])
+@pytest.mark.parametrize("N", [50, 20000, 200000])
+def test_distill_a_choice_of_one_costs_exactly_nothing(S, dtype, kind, N):
+    """One live entry among the listed, or one candidate: p = q = 1."""
+    g = torch.Generator().manual_seed(16)
+    s = (torch.randn((4, N), generator=g) * 5).to(dtype).cuda()
+    topk = torch.randint(0, N, (4, 3), generator=g, dtype=torch.int32).cuda()
+    topk[:, 1:] = -1
+    w = torch.rand((4, 3), generator=g).cuda() * 7 + 0.1
+    loss, grad = S.distill_topk(s, topk, w, teacher_kind=kind, over="listed", temperature=1.7)
+    assert not loss.any() and not grad.any()
+    topk[:] = 0
+    topk[:, 1:] = torch.tensor([1, 77], dtype=torch.int32)  # dead: there is one candidate
+    lens = torch.ones(4, dtype=torch.int32, device="cuda")
+    loss, grad = S.distill_topk(s, topk, w, lens=lens, teacher_kind=kind, temperature=0.3)
+    assert not loss.any() and not grad.any()
+
+
+@pytest.mark.parametrize("scope", ["candidates", "listed"])
+def test_distill_weights_of_any_size(S, scope):
+    s, lens, topk, w = case(17, 6, 3000, 40)
+    check(S, s, lens, topk, w * 1e36, scope=scope)
+    check(S, s, lens, topk, w * 1e-36, scope=scope)
+    s[:, ::3] = -math.inf
+    w[topk % 3 == 0] = 0.0
+    check(S, s, lens, topk, w, scope=scope)

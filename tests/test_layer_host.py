@@ -154,6 +154,7 @@ def test_distill_refusals(L):
                                   None)
     bad, uns = svt.SVT_ERR_INVALID_ARG, svt.SVT_ERR_UNSUPPORTED
     assert call(dt=2) == uns and call(N=1 << 30 | 1, st=1 << 31, ds=1 << 31) == uns
+    assert call(K=(1 << 30) + 1) == uns and call(T=(1 << 27) + 1) == uns
     assert call(T=-1) == bad and call(N=-1) == bad and call(K=0) == bad
     assert call(kind=2) == bad and call(scope=2) == bad
     for tau in (0.0, -1.0, float("nan"), float("inf"), 1e-7, 1e7):
