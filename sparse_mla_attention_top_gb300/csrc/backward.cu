@@ -5,9 +5,10 @@
 // and a cache row's gradient is the sum of dK (+ dV on the latent columns) over the lists that
 // hold it. sum over heads of P is each entry's attention weight.
 //
-// Three kernels. prepare resolves the lists, forms delta and zeroes the cache rows' sums. The main kernel walks (row-set, 64-entry tile) pairs, a row-set being up to 64 heads of
-// one query, one persistent CTA per SM with an equal share of all tiles (stream-K). finish joins the
-// dq of row-sets cut between CTAs (fp32, in a fixed order) and rounds the cache rows' sums to bf16.
+// Three kernels. prepare resolves the lists, forms delta and zeroes the cache rows' sums. The main
+// kernel walks (row-set, 64-entry tile) pairs, a row-set being up to 64 heads of one query, one
+// persistent CTA per SM with an equal share of all tiles (stream-K). finish joins the dq of row-sets
+// cut between CTAs (fp32, in a fixed order) and rounds the cache rows' sums to bf16.
 //
 // Main kernel, per tile, on tcgen05 with fp32 accumulators in tensor memory (e = entry, r = head
 // row, c = channel; the contractions' operands are the tiles as they lie, read K- or MN-major):
@@ -87,7 +88,9 @@ constexpr uint32_t kIdescKvRope = idesc_f32acc(64, 64, 1, 0, kFmtBf16);
 
 // Programmatic dependent launch: lets the next kernel of the stream begin; waits until the last one has
 // ended and its writes are visible.
-__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // The part of one row-set that this CTA walks: live tiles j0 .. j1 - 1 (none when j0 >= j1), starting
@@ -225,7 +228,8 @@ __device__ __forceinline__ void mma_role(const BackwardParams& p, uint8_t* smem,
   auto scores = [&](uint32_t g) -> bool {
     // the S^T and dP^T columns last held the previous tile's blocks 3 and 1
     if (!mbar_wait(bar(kBarKvFull), g & 1, wc)) return false;
-    if (g > 0 && !(mbar_wait(bar(kBarBlockFree + 1), (g - 1) & 1, wc) && mbar_wait(bar(kBarBlockFree + 3), (g - 1) & 1, wc)))
+    if (g > 0 && !(mbar_wait(bar(kBarBlockFree + 1), (g - 1) & 1, wc) &&
+                   mbar_wait(bar(kBarBlockFree + 3), (g - 1) & 1, wc)))
       return false;
     tc_fence_after();
 #pragma unroll 1
@@ -653,8 +657,8 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const BackwardPar
 }
 
 // CTAs below join_ctas join the dq of the row-set that the border before CTA c + 1 of the main
-// kernel cuts (the first such border of the row-set does it), 8 rows each; the others round
-// the cache rows' sums to bf16, eight values at a time.
+// kernel cuts (the first such border of the row-set does it), four rows each; the others round the
+// cache rows' sums to bf16, 32 channels a thread.
 constexpr int kJoinRows = 4;
 __global__ void __launch_bounds__(256) finish_kernel(const BackwardParams p, int join_ctas) {
   grid_wait();
