@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const BackwardPar
 
 // CTAs below join_ctas join the dq of the row-set that the border before CTA c + 1 of the main
 // kernel cuts (the first such border of the row-set does it), four rows each; the others round the
-// cache rows' sums to bf16, 32 channels a thread.
+// cache rows' sums to bf16.
 constexpr int kJoinRows = 4;
 __global__ void __launch_bounds__(256) finish_kernel(const BackwardParams p, int join_ctas) {
   grid_wait();
@@ -692,30 +692,31 @@ __global__ void __launch_bounds__(256) finish_kernel(const BackwardParams p, int
     }
     return;
   }
-  // a thread takes 32 channels, in the order of add_rows: eight 16-byte reads, four 16-byte writes
-  const long long n = p.num_slots * (kRow / 32), step = (gridDim.x - join_ctas) * 256ll;
-  for (long long i = (blockIdx.x - join_ctas) * 256ll + threadIdx.x; i < n; i += step) {
-    float4 v[8];
+  // 16 bytes of the sums hold four channels a stride apart (add_rows): neighbours exchange two each and
+  // write pairs
+  const long long n = p.num_slots * (kRow / 4), step = (gridDim.x - join_ctas) * 256ll;
+  const bool odd = (threadIdx.x & 1) != 0;
+  for (long long i = (blockIdx.x - join_ctas) * 256ll + threadIdx.x; i < n; i += 4 * step) {
+    float4 v[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = reinterpret_cast<const float4*>(p.dkv_acc)[8 * i + k];
-    uint4* dst = reinterpret_cast<uint4*>(p.dkv) + 4 * i;
-    if (i % (kRow / 32) < kVdim / 32) {
-      dst[0] = make_uint4(pack_bf16x2(v[0].x, v[1].x), pack_bf16x2(v[2].x, v[3].x), pack_bf16x2(v[4].x, v[5].x),
-                          pack_bf16x2(v[6].x, v[7].x));
-      dst[1] = make_uint4(pack_bf16x2(v[0].y, v[1].y), pack_bf16x2(v[2].y, v[3].y), pack_bf16x2(v[4].y, v[5].y),
-                          pack_bf16x2(v[6].y, v[7].y));
-      dst[2] = make_uint4(pack_bf16x2(v[0].z, v[1].z), pack_bf16x2(v[2].z, v[3].z), pack_bf16x2(v[4].z, v[5].z),
-                          pack_bf16x2(v[6].z, v[7].z));
-      dst[3] = make_uint4(pack_bf16x2(v[0].w, v[1].w), pack_bf16x2(v[2].w, v[3].w), pack_bf16x2(v[4].w, v[5].w),
-                          pack_bf16x2(v[6].w, v[7].w));
-    } else {
+    for (int u = 0; u < 4; ++u)
+      if (i + u * step < n) v[u] = reinterpret_cast<const float4*>(p.dkv_acc)[i + u * step];
 #pragma unroll
-      for (int h = 0; h < 8; h += 4) {
-        dst[h / 2] = make_uint4(pack_bf16x2(v[h].x, v[h + 1].x), pack_bf16x2(v[h + 2].x, v[h + 3].x),
-                                pack_bf16x2(v[h].y, v[h + 1].y), pack_bf16x2(v[h + 2].y, v[h + 3].y));
-        dst[h / 2 + 1] = make_uint4(pack_bf16x2(v[h].z, v[h + 1].z), pack_bf16x2(v[h + 2].z, v[h + 3].z),
-                                    pack_bf16x2(v[h].w, v[h + 1].w), pack_bf16x2(v[h + 2].w, v[h + 3].w));
-      }
+    for (int u = 0; u < 4; ++u) {
+      const long long at = i + u * step;
+      // (n and step are even: both lanes of a pair are here)
+      const unsigned pair = 3u << (threadIdx.x & 30);
+      if (at >= n) break;
+      const float a = __shfl_xor_sync(pair, odd ? v[u].x : v[u].z, 1);
+      const float b = __shfl_xor_sync(pair, odd ? v[u].y : v[u].w, 1);
+      const long long row = at / (kRow / 4);
+      const int c4 = static_cast<int>(at - row * (kRow / 4));
+      const bool rope = c4 >= kVdim / 4;
+      const int stride = rope ? 4 : 8, k = rope ? c4 - kVdim / 4 : c4;
+      const int first = (rope ? kVdim + 16 * (k >> 2) + (k & 3) : 32 * (k >> 3) + (k & 7)) - odd;
+      uint16_t* dst = p.dkv + row * kRow + first + (odd ? 2 * stride : 0);
+      *reinterpret_cast<uint32_t*>(dst) = odd ? pack_bf16x2(a, v[u].z) : pack_bf16x2(v[u].x, a);
+      *reinterpret_cast<uint32_t*>(dst + stride) = odd ? pack_bf16x2(b, v[u].w) : pack_bf16x2(v[u].y, b);
     }
   }
 }
@@ -760,7 +761,7 @@ cudaError_t launch_backward(const BackwardParams& p, const ListParams& l, cudaSt
   e = cudaLaunchKernelEx(&cfg, backward_kernel, p);
   if (e != cudaSuccess) return e;
   const int join = (p.num_ctas - 1) * (kRows / kJoinRows);
-  const long long n = (p.num_slots * (kRow / 32) + 255) / 256;
+  const long long n = (p.num_slots * (kRow / 4) + 1023) / 1024;
   cfg.gridDim = dim3(static_cast<unsigned>(join + (n < 1216 ? n : 1216)));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
