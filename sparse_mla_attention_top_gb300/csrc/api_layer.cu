@@ -73,7 +73,7 @@ BackwardWs backward_ws(const svt::BackwardParams& p) {
   BackwardWs w;
   w.slots = svt::kStatusBytes;
   w.live_len = w.slots + round_up(static_cast<size_t>(p.T) * p.K * 4, 256);
-  w.stats = w.live_len + round_up(static_cast<size_t>(p.T) * 4, 256);
+  w.stats = w.live_len + round_up(static_cast<size_t>(p.T) * p.chunks * 4, 256);
   w.part = w.stats + round_up(static_cast<size_t>(p.T) * p.H * 8, 256);
   w.acc = w.part + 2ull * p.num_ctas * 64 * svt::kRow * 4;
   w.end = w.acc + round_up(static_cast<size_t>(p.num_slots) * svt::kRow * 4, 256);

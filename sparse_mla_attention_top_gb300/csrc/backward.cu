@@ -129,7 +129,9 @@ struct SegIter {
     const int chunk = r - s.t * p.hchunks;
     s.base = static_cast<long long>(s.t) * p.H + chunk * kRows;
     s.nvalid = min(kRows, p.H - chunk * kRows);
-    const int live = (p.live_len[s.t] + kEntries - 1) / kEntries;
+    int reach = 0;
+    for (int i = 0; i < p.chunks; ++i) reach = max(reach, p.live_len[static_cast<long long>(s.t) * p.chunks + i]);
+    const int live = (reach + kEntries - 1) / kEntries;
     s.j0 = static_cast<int>(pos - first);
     s.j1 = min(static_cast<int>(end - first), live);
     s.turn = s.j0 < s.j1 ? static_cast<int>(static_cast<long long>(blockIdx.x) * (s.j1 - s.j0) / p.num_ctas) : 0;
@@ -570,25 +572,29 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const BackwardPar
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// CTAs 0 .. T - 1: a query's list as cache rows, and how far the live ones reach. The next delta_ctas,
+// The first T * chunks CTAs: 2048 entries of a query's list as cache rows, and how far the live ones
+// reach. The next delta_ctas,
 // 32 heads of any queries each: (lse, delta); a head without a live entry (lse = -inf)
 // gets +inf, so that P = 0. The others zero the cache rows' sums.
 constexpr int kPrepThreads = 256;
 constexpr int kPrepHeads = 32;
+constexpr int kListChunk = 2048;
 __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const BackwardParams p, const ListParams l,
                                                                int delta_ctas) {
   const int tid = threadIdx.x, lane = tid & 31;
   grid_launch_dependents();
-  if (static_cast<int>(blockIdx.x) < p.T) {
+  const int lists = p.T * p.chunks;
+  if (static_cast<int>(blockIdx.x) < lists) {
     __shared__ int reach;
-    const int t = blockIdx.x;
+    const int t = blockIdx.x / p.chunks, k0 = (blockIdx.x - t * p.chunks) * kListChunk;
+    const int k1 = min(p.K, k0 + kListChunk);
     if (tid == 0) reach = 0;
     __syncthreads();
     const ReqContext ctx = request_context(t, l.req_of_token, l.block_table, l.num_reqs, l.max_blocks, l.seq_lens);
     const int len = l.topk_len ? l.topk_len[t] : p.K;
     int err = 0, last = 0;
 #pragma unroll 4
-    for (int k = tid; k < p.K; k += kPrepThreads) {
+    for (int k = k0 + tid; k < k1; k += kPrepThreads) {
       const long long at = static_cast<long long>(t) * p.K + k;
       int slot = -1;
       if (k < len) {
@@ -604,12 +610,12 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const BackwardPar
     if (lane == 0 && last > 0) atomicMax(&reach, last);
     if (__any_sync(0xffffffffu, err != 0) && lane == 0) atomicOr(p.status, SVT_DEV_ERR_INDEX_RANGE);
     __syncthreads();
-    if (tid == 0) p.live_len[t] = reach;
+    if (tid == 0) p.live_len[blockIdx.x] = reach;
     return;
   }
-  const int cta = blockIdx.x - p.T;
+  const int cta = blockIdx.x - lists;
   if (cta >= delta_ctas) {
-    const long long n = p.num_slots * (kRow / 4), step = (gridDim.x - p.T - delta_ctas) * static_cast<long long>(kPrepThreads);
+    const long long n = p.num_slots * (kRow / 4), step = (gridDim.x - lists - delta_ctas) * static_cast<long long>(kPrepThreads);
     for (long long i = (cta - delta_ctas) * static_cast<long long>(kPrepThreads) + tid; i < n; i += step)
       reinterpret_cast<float4*>(p.dkv_acc)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     return;
@@ -726,6 +732,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const BackwardParams p, int
 void plan_backward(BackwardParams& p, int sms) {
   p.hchunks = (p.H + kRows - 1) / kRows;
   p.tiles = (p.K + kEntries - 1) / kEntries;
+  p.chunks = (p.K + kListChunk - 1) / kListChunk;
   p.total_tiles = static_cast<long long>(p.T) * p.hchunks * p.tiles;
   p.num_ctas = static_cast<int>(p.total_tiles < sms ? p.total_tiles : sms);
 }
@@ -742,7 +749,7 @@ cudaError_t launch_backward(const BackwardParams& p, const ListParams& l, cudaSt
   if (e != cudaSuccess) return e;
   const long long zero = (p.num_slots * (kRow / 4) + kPrepThreads - 1) / kPrepThreads;
   const int delta_ctas = static_cast<int>((static_cast<long long>(p.T) * p.H + kPrepHeads - 1) / kPrepHeads);
-  prepare_kernel<<<static_cast<unsigned>(p.T + delta_ctas + (zero < 1216 ? zero : 1216)), kPrepThreads, 0, stream>>>(
+  prepare_kernel<<<static_cast<unsigned>(p.T * p.chunks + delta_ctas + (zero < 1216 ? zero : 1216)), kPrepThreads, 0, stream>>>(
       p, l, delta_ctas);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

@@ -263,15 +263,16 @@ struct BackwardParams {
   float* weights;  // [T, K] or null
   // scratch
   int32_t* slots;     // [T, K] resolved, -1 = dead
-  int32_t* live_len;  // [T] entries up to the last live one
+  int32_t* live_len;  // [T, chunks] entries up to the chunk's last live one (0: it has none)
   float2* stats;      // [T, H]: lse (+inf for a head with no live entry), delta
   float* dq_part;     // [2 * num_ctas, 64, 576]: dq of row-sets cut between CTAs
   float* dkv_acc;     // [num_slots, 576]
   int* status;
   unsigned long long wait_limit_ns;  // 0 = the default
   int fault;                         // planted faults (kFault* bits)
-  // schedule (plan_backward): 64-head chunks per query, 64-entry tiles per row-set
-  int hchunks, tiles, num_ctas;
+  // schedule (plan_backward): 64-head chunks per query, 64-entry tiles per row-set, the pieces in which
+  // a list is resolved
+  int hchunks, tiles, chunks, num_ctas;
   long long total_tiles;
 };
 // How the lists resolve to cache rows.

@@ -85,6 +85,16 @@ def test_backward_more_queries_than_sms(S, T, H, K):
     check(S, normal(1, T, H, 576), normal(2, 700, 576), lists(3, T, K, 700), normal(4, T, H, 512))
 
 
+@pytest.mark.parametrize("T,H,K,live", [(1, 4, 9000, 9000), (2, 16, 5000, 2049), (3, 1, 4097, 1), (2, 70, 4096, 0)])
+def test_backward_lists_of_several_pieces(S, T, H, K, live):
+    """Long lists, their live entries ending in any piece of them (or missing, or only at the very end)."""
+    slots = lists(98, T, K, 9500, dead=0.0)
+    slots[:, live:] = -1
+    if live == 1:
+        slots[0, 0], slots[0, K - 1] = -1, 77
+    check(S, normal(99, T, H, 576), normal(100, 9500, 576), slots, normal(101, T, H, 512))
+
+
 def test_backward_paged_requests_counts_and_padded_rows(S):
     T, H, K, P = 6, 12, 40, 16
     n = 10 * P
