@@ -45,44 +45,76 @@ constexpr int kRows = 64;     // heads of a row-set
 constexpr int kEntries = 64;  // list entries of a tile
 constexpr float kLog2e = 1.4426950408889634f;
 
-// shared memory (bytes from a 1024-byte boundary): 64 x 64 bf16 blocks in the 128-byte swizzle
-constexpr uint32_t kBlk = 8192;
-constexpr uint32_t kOffQ = 0;            // q0 dout0 q1 dout1 .. q7 dout7 q8
-constexpr uint32_t kOffKv = 17 * kBlk;   // 9 blocks
-constexpr uint32_t kOffP = kOffKv + 9 * kBlk;
-constexpr uint32_t kOffDs = kOffP + kBlk;
-constexpr uint32_t kOffMisc = kOffDs + kBlk;
+constexpr uint32_t kBlk = 8192;  // 64 x 64 bf16 in the 128-byte swizzle
 struct Misc {
   int slot[4][kEntries];  // the tile's cache rows, a ring: scatter may trail the gather by two tiles
   float weight[2][kEntries];
-  uint64_t bars[20];
+  uint64_t bars[22];
   uint32_t tmem;
   int abort_flag;
 };
-constexpr uint32_t kSmem = kOffMisc + sizeof(Misc) + 1024;
-static_assert(kSmem <= 232448, "backward shared memory");
 
 // barriers
-enum { kBarKvFull, kBarKvFree, kBarS, kBarP, kBarPFree, kBarSeg, kBarDq, kBarDqFree, kBarBlock,
-       kBarBlockFree = kBarBlock + 5, kBarDone = kBarBlockFree + 5, kNumBars };
-static_assert(kNumBars <= 20, "barriers");
+enum { kBarKvFull, kBarKvFree = kBarKvFull + 2, kBarS = kBarKvFree + 2, kBarP, kBarPFree, kBarSeg, kBarDq, kBarDqFree,
+       kBarBlock, kBarBlockFree = kBarBlock + 5, kBarDone = kBarBlockFree + 5, kNumBars };
+static_assert(kNumBars <= 22, "barriers");
 
-// tensor memory columns: dq^T in five blocks of 64 (channels 128 mb .. +127, then the 64 rope
-// ones), S^T, dP^T, and a block of dKV^T. The S^T columns hold blocks 0 and 3 of dKV^T and the dP^T
-// columns block 1 once the softmax has read them; the others go to the last columns
-constexpr uint32_t kTmDq = 0, kTmS = 320, kTmDp = kTmS + 64, kTmX = kTmDp + 64;
+// Shared memory (bytes from a 1024-byte boundary) and tensor memory (columns) for row-sets of R heads,
+// R = 64 or 32. Tensor memory: dq^T in five blocks of R (channels 128 mb .. +127, then the 64 rope ones),
+// S^T, dP^T, blocks of dKV^T.
+template <int R>
+struct Lay;
+
+// R = 64: q0 dout0 q1 dout1 .. q7 dout7 q8, one tile of rows. The S^T columns hold blocks 0 and 3 of dKV^T
+// and the dP^T columns block 1 once the softmax has read them; the others go to the last 64.
+template <>
+struct Lay<64> {
+  static constexpr uint32_t kQBlocks = 17, kKvBufs = 1;
+  static constexpr uint32_t kTmS = 320, kTmDp = kTmS + 64;
+  static __device__ constexpr uint32_t block(int cb) { return cb == 1 ? kTmDp : (cb == 2 || cb == 4 ? kTmDp + 64 : kTmS); }
+};
+// R = 32: a block's rows are 32 heads of q, then the same of dout (the last block: rows 32 .. 63 unused),
+// which leaves room for a second tile of rows; and blocks 0 to 3 have columns of their own (block 4: block
+// 1's, as the same warps drain both), so that a tile's additions run beside the next tile's products.
+template <>
+struct Lay<32> {
+  static constexpr uint32_t kQBlocks = 9, kKvBufs = 2;
+  static constexpr uint32_t kTmS = 160, kTmDp = kTmS + 32;
+  static __device__ constexpr uint32_t block(int cb) { return kTmS + 64 + 64 * (cb == 4 ? 1 : cb); }
+};
+constexpr uint32_t kTmDq = 0, kOffQ = 0;
+template <int R>
+constexpr uint32_t kOffKv = Lay<R>::kQBlocks* kBlk;  // 9 blocks a tile
+template <int R>
+constexpr uint32_t kOffP = kOffKv<R> + Lay<R>::kKvBufs * 9 * kBlk;  // 64 entries x R heads
+template <int R>
+constexpr uint32_t kOffDs = kOffP<R> + 128 * R;
+template <int R>
+constexpr uint32_t kOffMisc = kOffDs<R> + 128 * R;
+template <int R>
+constexpr uint32_t kSmem = kOffMisc<R> + sizeof(Misc) + 1024;
+static_assert(kSmem<64> <= 232448 && kSmem<32> <= 232448, "backward shared memory");
+
+// The 16-byte chunk of a row of 64 bytes in the 64-byte swizzle.
+__device__ __forceinline__ uint32_t sw64_offset(uint32_t row, uint32_t chunk) {
+  return row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
+}
 
 constexpr int kSoftWarps = 8, kScatWarps = 8, kFillWarps = 3;
 constexpr int kScatWarp0 = kSoftWarps, kFillWarp0 = kScatWarp0 + kScatWarps, kMmaWarp = kFillWarp0 + kFillWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kFillThreads = 32 * kFillWarps;
 constexpr int kFillStep = kFillThreads / 8;                       // rows filled at once, 8 threads each
-constexpr int kFillRows = (kRows + kFillStep - 1) / kFillStep;  // rows per thread
+constexpr int kFillRows = (kEntries + kFillStep - 1) / kFillStep;  // rows per thread
 
-constexpr uint32_t kIdescS = idesc_f32acc(64, 128, 0, 0, kFmtBf16);
-constexpr uint32_t kIdescSRope = idesc_f32acc(64, 64, 0, 0, kFmtBf16);
-constexpr uint32_t kIdescDq = idesc_f32acc(128, 64, 1, 1, kFmtBf16);
-constexpr uint32_t kIdescDqRope = idesc_f32acc(64, 64, 1, 1, kFmtBf16);
+template <int R>
+constexpr uint32_t kIdescS = idesc_f32acc(64, 2 * R, 0, 0, kFmtBf16);
+template <int R>
+constexpr uint32_t kIdescSRope = idesc_f32acc(64, R, 0, 0, kFmtBf16);
+template <int R>
+constexpr uint32_t kIdescDq = idesc_f32acc(128, R, 1, 1, kFmtBf16);
+template <int R>
+constexpr uint32_t kIdescDqRope = idesc_f32acc(64, R, 1, 1, kFmtBf16);
 constexpr uint32_t kIdescKv = idesc_f32acc(128, 64, 1, 0, kFmtBf16);
 constexpr uint32_t kIdescKvRope = idesc_f32acc(64, 64, 1, 0, kFmtBf16);
 
@@ -142,6 +174,7 @@ struct SegIter {
   }
 };
 
+template <int R>
 __device__ __forceinline__ void gather_role(const BackwardParams& p, uint8_t* smem, Misc* misc, uint32_t bars,
                                             const WaitCtl& wc) {
   const int tid = static_cast<int>(threadIdx.x) - 32 * kFillWarp0;
@@ -155,17 +188,19 @@ __device__ __forceinline__ void gather_role(const BackwardParams& p, uint8_t* sm
     if (s.j0 >= s.j1) continue;
     // the last segment's products are done: q and dout may be replaced
     if (segs > 0) mbar_wait(bar(kBarSeg), (segs - 1) & 1, wc);
-    for (int r = r0; r < kRows; r += kFillStep) {
+    for (int r = r0; r < R; r += kFillStep) {
       const uint32_t ok = r < s.nvalid ? 16u : 0u;
       const uint16_t* q = p.q + (s.base + (ok ? r : 0)) * kRow + c * 8;
       const uint16_t* d = p.dout + (s.base + (ok ? r : 0)) * kVdim + c * 8;
       const uint32_t at = base + kOffQ + sw128_offset(r, c);
+      constexpr uint32_t kStep = (Lay<R>::kQBlocks - 1) / 8 * kBlk;
+      constexpr uint32_t kDout = R == 64 ? kBlk : R * 128;  // from a row of q to dout's
 #pragma unroll
       for (int kb = 0; kb < 8; ++kb) {
-        cp_async16(at + 2 * kb * kBlk, q + 64 * kb, ok);
-        cp_async16(at + (2 * kb + 1) * kBlk, d + 64 * kb, ok);
+        cp_async16(at + kb * kStep, q + 64 * kb, ok);
+        cp_async16(at + kb * kStep + kDout, d + 64 * kb, ok);
       }
-      cp_async16(at + 16 * kBlk, q + 512, ok);
+      cp_async16(at + 8 * kStep, q + 512, ok);
     }
     const int32_t* list = p.slots + static_cast<long long>(s.t) * p.K;
     int slot[kFillRows];
@@ -178,14 +213,16 @@ __device__ __forceinline__ void gather_role(const BackwardParams& p, uint8_t* sm
     };
     load_slots(s.tile(s.j0));
     for (int j = s.j0; j < s.j1; ++j, ++g) {
-      if (j > s.j0) mbar_wait(bar(kBarKvFree), (g - 1) & 1, wc);
+      constexpr uint32_t kBufs = Lay<R>::kKvBufs;
+      const uint32_t buf = g % kBufs;
+      if (g >= kBufs) mbar_wait(bar(kBarKvFree + static_cast<int>(buf)), (g / kBufs - 1) & 1, wc);
 #pragma unroll
       for (int i = 0; i < kFillRows; ++i) {
         const int r = r0 + kFillStep * i;
         if (r >= kEntries) break;
         const uint32_t ok = slot[i] >= 0 ? 16u : 0u;
         const uint8_t* row = p.kv + (ok ? slot[i] * p.row_stride : 0) + c * 16;
-        const uint32_t at = base + kOffKv + sw128_offset(r, c);
+        const uint32_t at = base + kOffKv<R> + buf * 9 * kBlk + sw128_offset(r, c);
 #pragma unroll
         for (int kb = 0; kb < 9; ++kb) cp_async16(at + kb * kBlk, row + 128 * kb, ok);
         if (c == 0) misc->slot[g & 3][r] = slot[i];
@@ -193,7 +230,7 @@ __device__ __forceinline__ void gather_role(const BackwardParams& p, uint8_t* sm
       if (j + 1 < s.j1) load_slots(s.tile(j + 1));
       cp_async_wait_all();
       fence_proxy_async_smem();  // the rows (generic proxy) -> MMA operand reads
-      if (!(g == 0 && (p.fault & kFaultWithholdFirstFill))) mbar_arrive(bar(kBarKvFull));
+      if (!(g == 0 && (p.fault & kFaultWithholdFirstFill))) mbar_arrive(bar(kBarKvFull + static_cast<int>(buf)));
     }
     ++segs;
   }
@@ -218,13 +255,14 @@ __device__ __forceinline__ void umma_x4(uint32_t d, uint64_t a, uint64_t b, bool
 // while the next rows land, the next tile's S^T and dP^T, the last block. The issue has to keep up
 // with products of 32 to 64 cycles: one elected lane of a uniform warp (a lane chosen by its number:
 // 70 cycles an MMA, elected: 45), descriptors that advance by constants, loops of a few MMAs.
-__device__ __forceinline__ void mma_role(const BackwardParams& p, uint8_t* smem, uint32_t tmem, uint32_t bars,
-                                         const WaitCtl& wc) {
+__device__ __forceinline__ void mma_role64(const BackwardParams& p, uint8_t* smem, uint32_t tmem, uint32_t bars,
+                                           const WaitCtl& wc) {
+  using L = Lay<64>;
   const uint32_t base = smem_u32(smem);
   const uint64_t q_k = smem_desc_sw128(base + kOffQ, 16, 1024), q_mn = smem_desc_sw128(base + kOffQ, 2 * kBlk, 1024);
-  const uint64_t kv_k = smem_desc_sw128(base + kOffKv, 16, 1024), kv_mn = smem_desc_sw128(base + kOffKv, kBlk, 1024);
-  const uint64_t p_k = smem_desc_sw128(base + kOffP, 16, 1024), ds_k = smem_desc_sw128(base + kOffDs, 16, 1024);
-  const uint64_t ds_mn = smem_desc_sw128(base + kOffDs, kBlk, 1024);
+  const uint64_t kv_k = smem_desc_sw128(base + kOffKv<64>, 16, 1024), kv_mn = smem_desc_sw128(base + kOffKv<64>, kBlk, 1024);
+  const uint64_t p_k = smem_desc_sw128(base + kOffP<64>, 16, 1024), ds_k = smem_desc_sw128(base + kOffDs<64>, 16, 1024);
+  const uint64_t ds_mn = smem_desc_sw128(base + kOffDs<64>, kBlk, 1024);
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
   uint32_t segs = 0;
   auto scores = [&](uint32_t g) -> bool {
@@ -236,8 +274,8 @@ __device__ __forceinline__ void mma_role(const BackwardParams& p, uint8_t* smem,
     tc_fence_after();
 #pragma unroll 1
     for (uint32_t kb = 0; kb < 8; ++kb)
-      umma_x4<kIdescS, 32, 32>(tmem + kTmS, kv_k + kb * (kBlk >> 4), q_k + kb * (2 * kBlk >> 4), kb > 0);
-    umma_x4<kIdescSRope, 32, 32>(tmem + kTmS, kv_k + 8 * (kBlk >> 4), q_k + 16 * (kBlk >> 4), true);
+      umma_x4<kIdescS<64>, 32, 32>(tmem + L::kTmS, kv_k + kb * (kBlk >> 4), q_k + kb * (2 * kBlk >> 4), kb > 0);
+    umma_x4<kIdescSRope<64>, 32, 32>(tmem + L::kTmS, kv_k + 8 * (kBlk >> 4), q_k + 16 * (kBlk >> 4), true);
     umma_commit(bar(kBarS));
     return true;
   };
@@ -256,8 +294,8 @@ __device__ __forceinline__ void mma_role(const BackwardParams& p, uint8_t* smem,
       tc_fence_after();
 #pragma unroll 1
       for (uint32_t mb = 0; mb < 4; ++mb)
-        umma_x4<kIdescDq, 2048, 2048>(tmem + kTmDq + 64 * mb, kv_mn + mb * (2 * kBlk >> 4), ds_mn, j > s.j0);
-      umma_x4<kIdescDqRope, 2048, 2048>(tmem + kTmDq + 256, kv_mn + 8 * (kBlk >> 4), ds_mn, j > s.j0);
+        umma_x4<kIdescDq<64>, 2048, 2048>(tmem + kTmDq + 64 * mb, kv_mn + mb * (2 * kBlk >> 4), ds_mn, j > s.j0);
+      umma_x4<kIdescDqRope<64>, 2048, 2048>(tmem + kTmDq + 256, kv_mn + 8 * (kBlk >> 4), ds_mn, j > s.j0);
       umma_commit(bar(kBarKvFree));
 #pragma unroll 1
       for (uint32_t cb = 0; cb < 4; ++cb) {
@@ -266,7 +304,7 @@ __device__ __forceinline__ void mma_role(const BackwardParams& p, uint8_t* smem,
         if (cb == 3) ok = mbar_wait(bar(kBarBlockFree), g & 1, wc);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + (cb == 1 ? kTmDp : (cb == 2 ? kTmX : kTmS));
+        const uint32_t d = tmem + L::block(static_cast<int>(cb));
         umma_x4<kIdescKv, 2048, 32>(d, q_mn + cb * (4 * kBlk >> 4), ds_k, false, steps);
         umma_x4<kIdescKv, 2048, 32>(d, q_mn + cb * (4 * kBlk >> 4) + (kBlk >> 4), p_k, true, steps);
         umma_commit(bar(kBarBlock + static_cast<int>(cb)));
@@ -275,7 +313,79 @@ __device__ __forceinline__ void mma_role(const BackwardParams& p, uint8_t* smem,
       if (ok) ok = mbar_wait(bar(kBarBlockFree + 2), g & 1, wc);
       if (!ok) break;
       tc_fence_after();
-      umma_x4<kIdescKvRope, 2048, 32>(tmem + kTmX, q_mn + 16 * (kBlk >> 4), ds_k, false, steps);
+      umma_x4<kIdescKvRope, 2048, 32>(tmem + L::block(4), q_mn + 16 * (kBlk >> 4), ds_k, false, steps);
+      umma_commit(bar(kBarBlock + 4));
+      umma_commit(bar(kBarPFree));
+    }
+    umma_commit(bar(kBarSeg));
+    umma_commit(bar(kBarDq));
+    ++segs;
+  }
+  umma_commit(bar(kBarDone));
+  mbar_wait_ignoring_abort(bar(kBarDone), 0, wc);  // nothing runs when tensor memory is released
+}
+
+// The same for row-sets of 32 heads. Per tile: four blocks of dKV, the next tile's S^T and dP^T (its rows have
+// a buffer of their own), dq, the last block.
+__device__ __forceinline__ void mma_role32(const BackwardParams& p, uint8_t* smem, uint32_t tmem, uint32_t bars,
+                                           const WaitCtl& wc) {
+  using L = Lay<32>;
+  const uint32_t base = smem_u32(smem);
+  const uint64_t q_k = smem_desc_sw128(base + kOffQ, 16, 1024), q_mn = smem_desc_sw128(base + kOffQ, kBlk, 1024);
+  const uint64_t kv_k0 = smem_desc_sw128(base + kOffKv<32>, 16, 1024);
+  const uint64_t kv_mn0 = smem_desc_sw128(base + kOffKv<32>, kBlk, 1024);
+  const uint64_t p_k = smem_desc_sw64(base + kOffP<32>, 16, 512), ds_k = smem_desc_sw64(base + kOffDs<32>, 16, 512);
+  const uint64_t ds_mn = smem_desc_sw64(base + kOffDs<32>, 4096, 512);
+  constexpr uint64_t kDout = 32 * 128 >> 4;  // from q's rows of a block to dout's
+  auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
+  auto scores = [&](uint32_t g) -> bool {
+    const uint32_t buf = g & 1;
+    // (the softmax has read the last S^T and dP^T: it has arrived with their P and dS)
+    if (!mbar_wait(bar(kBarKvFull + static_cast<int>(buf)), (g >> 1) & 1, wc)) return false;
+    tc_fence_after();
+    const uint64_t kv_k = kv_k0 + buf * (9 * kBlk >> 4);
+#pragma unroll 1
+    for (uint32_t kb = 0; kb < 8; ++kb)
+      umma_x4<kIdescS<32>, 32, 32>(tmem + L::kTmS, kv_k + kb * (kBlk >> 4), q_k + kb * (kBlk >> 4), kb > 0);
+    umma_x4<kIdescSRope<32>, 32, 32>(tmem + L::kTmS, kv_k + 8 * (kBlk >> 4), q_k + 8 * (kBlk >> 4), true);
+    umma_commit(bar(kBarS));
+    return true;
+  };
+  uint32_t g = 0, segs = 0;
+  bool ok = true;
+  SegIter it(p);
+  Seg s;
+  while (ok && it.next(s)) {
+    if (s.j0 >= s.j1) continue;
+    ok = scores(g);
+    const int steps = (s.nvalid + 15) / 16;  // rows past the last head add nothing to dKV
+    for (int j = s.j0; ok && j < s.j1; ++j, ++g) {
+      ok = mbar_wait(bar(kBarP), g & 1, wc);
+#pragma unroll 1
+      for (uint32_t cb = 0; ok && cb < 4; ++cb) {
+        // the last tile's block in these columns has been read
+        if (g > 0) ok = mbar_wait(bar(kBarBlockFree + static_cast<int>(cb == 1 ? 4 : cb)), (g - 1) & 1, wc);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + L::block(static_cast<int>(cb));
+        umma_x4<kIdescKv, 2048, 32>(d, q_mn + cb * (2 * kBlk >> 4), ds_k, false, steps);
+        umma_x4<kIdescKv, 2048, 32>(d, q_mn + cb * (2 * kBlk >> 4) + kDout, p_k, true, steps);
+        umma_commit(bar(kBarBlock + static_cast<int>(cb)));
+      }
+      if (ok && j + 1 < s.j1) ok = scores(g + 1);
+      if (ok && j == s.j0 && segs > 0) ok = mbar_wait(bar(kBarDqFree), (segs - 1) & 1, wc);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t kv_mn = kv_mn0 + (g & 1) * (9 * kBlk >> 4);
+#pragma unroll 1
+      for (uint32_t mb = 0; mb < 4; ++mb)
+        umma_x4<kIdescDq<32>, 2048, 1024>(tmem + kTmDq + 32 * mb, kv_mn + mb * (2 * kBlk >> 4), ds_mn, j > s.j0);
+      umma_x4<kIdescDqRope<32>, 2048, 1024>(tmem + kTmDq + 128, kv_mn + 8 * (kBlk >> 4), ds_mn, j > s.j0);
+      umma_commit(bar(kBarKvFree + static_cast<int>(g & 1)));
+      ok = mbar_wait(bar(kBarBlockFree + 1), g & 1, wc);
+      if (!ok) break;
+      tc_fence_after();
+      umma_x4<kIdescKvRope, 2048, 32>(tmem + L::block(4), q_mn + 8 * (kBlk >> 4), ds_k, false, steps);
       umma_commit(bar(kBarBlock + 4));
       umma_commit(bar(kBarPFree));
     }
@@ -349,18 +459,22 @@ __device__ __forceinline__ void add_rows(float* dst, const int* slots, const uin
   }
 }
 
+template <int R>
 __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* smem, Misc* misc, uint32_t tmem,
                                              uint32_t bars, const WaitCtl& wc) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3, half = warp >> 2;
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
   // S^T and dP^T (64 entries in lanes 0-15 of each quadrant): this thread's entries e and e + 8, and
-  // their heads 32 half + 8 k + 2 (lane & 3) and the next, k < 4
+  // their heads kHeads half + 8 k + 2 (lane & 3) and the next, k < kOcts
+  constexpr int kHeads = R / 2, kOcts = kHeads / 8;
   const int e = 16 * quad + (lane >> 2), pair = lane & 3;
   const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
-  // where this lane's row of the stored 8 x 8 matrices goes: matrix lane >> 3 is chunk 4 half + that
-  const uint32_t at0 = smem_u32(smem) + sw128_offset(16 * quad + (lane & 7), 4 * half + (lane >> 3));
-  const uint32_t at8 = at0 + 8 * 128;
+  // where this lane's row of the stored 8 x 8 matrices goes: matrix lane >> 3 is chunk 4 half + that, of
+  // entries e; with R = 32 chunks 2 half and 2 half + 1 of entries e, then of entries e + 8
+  const uint32_t at0 = smem_u32(smem) + (R == 64 ? sw128_offset(16 * quad + (lane & 7), 4 * half + (lane >> 3))
+                                                 : sw64_offset(16 * quad + 8 * (lane >> 4) + (lane & 7),
+                                                               2 * half + ((lane >> 3) & 1)));
   // an entry's weight: the two warps of a quadrant hold half of the heads each. Lanes 0 and 1 of four
   // keep the sums of e and e + 8
   const int we = e + 8 * (pair & 1);
@@ -371,10 +485,10 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
     const bool any = s.j0 < s.j1;
     // the exponent S - lse is one fma and takes its factor log2 e afterwards: lse in log2 units would be
     // off by 2^-24 of itself, here the rounding is relative to the difference
-    float lse[8], delta[8];  // delta times the softmax scale
+    float lse[2 * kOcts], delta[2 * kOcts];  // delta times the softmax scale
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 32 * half + 8 * (i >> 1) + 2 * pair + (i & 1);
+    for (int i = 0; i < 2 * kOcts; ++i) {
+      const int r = kHeads * half + 8 * (i >> 1) + 2 * pair + (i & 1);
       const float2 v = r < s.nvalid ? p.stats[s.base + r] : make_float2(CUDART_INF_F, 0.f);
       lse[i] = v.x;
       delta[i] = v.y * p.scale;
@@ -396,15 +510,15 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
     for (int j = s.j0; j < s.j1; ++j, ++g) {
       mbar_wait(bar(kBarS), g & 1, wc);
       tc_fence_after();
-      uint32_t sv[16], dv[16];
-      tmem_ld_16x256b_x4(lanes + kTmS + 32 * half, sv);
-      tmem_ld_16x256b_x4(lanes + kTmDp + 32 * half, dv);
+      uint32_t sv[4 * kOcts], dv[4 * kOcts];
+      tmem_ld_16x256b(lanes + Lay<R>::kTmS + kHeads * half, sv);
+      tmem_ld_16x256b(lanes + Lay<R>::kTmDp + kHeads * half, dv);
       const bool live0 = misc->slot[g & 3][e] >= 0, live8 = misc->slot[g & 3][e + 8] >= 0;
       tmem_ld_wait();
-      uint32_t pp[8], pd[8];  // [2 k]: entry e, [2 k + 1]: entry e + 8
+      uint32_t pp[2 * kOcts], pd[2 * kOcts];  // [2 k]: entry e, [2 k + 1]: entry e + 8
       float w0 = 0.f, w8 = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < kOcts; ++k)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float pr[2], d[2];
@@ -423,10 +537,16 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
         }
       // the last tile's products with P and dS are done
       if (g > 0) mbar_wait(bar(kBarPFree), (g - 1) & 1, wc);
-      stmatrix_x4(at0 + kOffP, pp[0], pp[2], pp[4], pp[6]);
-      stmatrix_x4(at8 + kOffP, pp[1], pp[3], pp[5], pp[7]);
-      stmatrix_x4(at0 + kOffDs, pd[0], pd[2], pd[4], pd[6]);
-      stmatrix_x4(at8 + kOffDs, pd[1], pd[3], pd[5], pd[7]);
+      if constexpr (R == 64) {
+        const uint32_t at8 = at0 + 8 * 128;
+        stmatrix_x4(at0 + kOffP<R>, pp[0], pp[2], pp[4], pp[6]);
+        stmatrix_x4(at8 + kOffP<R>, pp[1], pp[3], pp[5], pp[7]);
+        stmatrix_x4(at0 + kOffDs<R>, pd[0], pd[2], pd[4], pd[6]);
+        stmatrix_x4(at8 + kOffDs<R>, pd[1], pd[3], pd[5], pd[7]);
+      } else {
+        stmatrix_x4(at0 + kOffP<R>, pp[0], pp[2], pp[1], pp[3]);
+        stmatrix_x4(at0 + kOffDs<R>, pd[0], pd[2], pd[1], pd[3]);
+      }
       if (p.weights != nullptr) {
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
@@ -448,40 +568,41 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
         if (cb == 0 && p.weights != nullptr) put_weight(j);
         tc_fence_after();
         uint32_t v[32];
-        tmem_ld32(lanes + kTmS + 32 * half, v);
+        tmem_ld32(lanes + Lay<R>::block(cb) + 32 * half, v);
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(bar(kBarBlockFree + cb));
         add_rows<false>(p.dkv_acc + 128 * cb + 32 * quad, misc->slot[g & 3] + 32 * half, v);
       }
     }
-    // dq^T: lane = channel, this warp's heads 32 half .. + 31
+    // dq^T: lane = channel, this warp's heads kHeads half and on
     if (any) {
       mbar_wait(bar(kBarDq), segs & 1, wc);
       tc_fence_after();
     }
 #pragma unroll 1
     for (int mb = 0; mb < 5; ++mb) {
-      uint32_t v[32];
+      uint32_t v[kHeads];
       if (any) {
-        tmem_ld32(lanes + kTmDq + 64 * mb + 32 * half, v);
+        if constexpr (R == 64) tmem_ld32(lanes + kTmDq + R * mb + kHeads * half, v);
+        else tmem_ld16(lanes + kTmDq + R * mb + kHeads * half, v);
         tmem_ld_wait();
       } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0u;
+        for (int i = 0; i < kHeads; ++i) v[i] = 0u;
       }
       if (mb == 4 && lane >= 16) continue;
       const int c = 128 * mb + (mb < 4 ? 32 : 16) * quad + lane;
       if (s.whole) {
-        uint16_t* dst = p.dq + (s.base + 32 * half) * kRow + c;
+        uint16_t* dst = p.dq + (s.base + kHeads * half) * kRow + c;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (32 * half + i < s.nvalid) dst[i * kRow] = static_cast<uint16_t>(pack_bf16x2(__uint_as_float(v[i]), 0.f));
+        for (int i = 0; i < kHeads; ++i)
+          if (kHeads * half + i < s.nvalid) dst[i * kRow] = static_cast<uint16_t>(pack_bf16x2(__uint_as_float(v[i]), 0.f));
       } else {
-        float* dst = p.dq_part + (static_cast<long long>(s.part) * kRows + 32 * half) * kRow + c;
+        float* dst = p.dq_part + (static_cast<long long>(s.part) * kRows + kHeads * half) * kRow + c;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (32 * half + i < s.nvalid) dst[i * kRow] = __uint_as_float(v[i]);
+        for (int i = 0; i < kHeads; ++i)
+          if (kHeads * half + i < s.nvalid) dst[i * kRow] = __uint_as_float(v[i]);
       }
     }
     if (any) {
@@ -492,6 +613,7 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
   }
 }
 
+template <int R>
 __device__ __forceinline__ void scatter_role(const BackwardParams& p, Misc* misc, uint32_t tmem, uint32_t bars,
                                              const WaitCtl& wc) {
   const int warp = (threadIdx.x >> 5) - kScatWarp0, lane = threadIdx.x & 31;
@@ -506,7 +628,7 @@ __device__ __forceinline__ void scatter_role(const BackwardParams& p, Misc* misc
     for (int j = s.j0; j < s.j1; ++j, ++g) {
 #pragma unroll 1
       for (int cb = 1 + group; cb < 5; cb += 3) {
-        const uint32_t from = cb == 1 ? kTmDp : kTmX;
+        const uint32_t from = Lay<R>::block(cb);
         if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarBlock + cb), g & 1, wc))) return;
         tc_fence_after();
         uint32_t v[2][32];
@@ -528,16 +650,17 @@ __device__ __forceinline__ void scatter_role(const BackwardParams& p, Misc* misc
   }
 }
 
+template <int R>
 __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const BackwardParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  Misc* misc = reinterpret_cast<Misc*>(smem + kOffMisc);
+  Misc* misc = reinterpret_cast<Misc*>(smem + kOffMisc<R>);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // a uniform value
   const uint32_t bars = smem_u32(misc->bars);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       int count = 1;
-      if (i == kBarKvFull) count = kFillThreads;
+      if (i < kBarKvFree) count = kFillThreads;
       if (i == kBarP || i == kBarDqFree) count = 32 * kSoftWarps;
       if (i >= kBarBlockFree && i < kBarBlockFree + 5) count = 128;
       if (i == kBarBlockFree || i == kBarBlockFree + 3) count = 32 * kSoftWarps;
@@ -558,13 +681,14 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const BackwardPar
   grid_launch_dependents();
   grid_wait();  // for prepare_kernel, beside whose end the above ran
   if (warp < kScatWarp0) {
-    softmax_role(p, smem, misc, tmem, bars, wc);
+    softmax_role<R>(p, smem, misc, tmem, bars, wc);
   } else if (warp < kFillWarp0) {
-    scatter_role(p, misc, tmem, bars, wc);
+    scatter_role<R>(p, misc, tmem, bars, wc);
   } else if (warp < kMmaWarp) {
-    gather_role(p, smem, misc, bars, wc);
+    gather_role<R>(p, smem, misc, bars, wc);
   } else if (elect_one()) {
-    mma_role(p, smem, tmem, bars, wc);
+    if constexpr (R == 64) mma_role64(p, smem, tmem, bars, wc);
+    else mma_role32(p, smem, tmem, bars, wc);
   }
   tc_fence_before();
   __syncthreads();
@@ -745,7 +869,10 @@ cudaError_t launch_backward(const BackwardParams& p, const ListParams& l, cudaSt
     if (e != cudaSuccess) return e;
   }
   if (!any) return cudaMemsetAsync(p.dkv, 0, static_cast<size_t>(p.num_slots) * kRow * sizeof(uint16_t), stream);
-  e = cudaFuncSetAttribute(backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const bool packed = p.H <= 32;
+  const auto kernel = packed ? backward_kernel<32> : backward_kernel<64>;
+  const uint32_t smem = packed ? kSmem<32> : kSmem<64>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const long long zero = (p.num_slots * (kRow / 4) + kPrepThreads - 1) / kPrepThreads;
   const int delta_ctas = static_cast<int>((static_cast<long long>(p.T) * p.H + kPrepHeads - 1) / kPrepHeads);
@@ -764,8 +891,8 @@ cudaError_t launch_backward(const BackwardParams& p, const ListParams& l, cudaSt
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(p.num_ctas));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  e = cudaLaunchKernelEx(&cfg, backward_kernel, p);
+  cfg.dynamicSmemBytes = smem;
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess) return e;
   const int join = (p.num_ctas - 1) * (kRows / kJoinRows);
   const long long n = (p.num_slots * (kRow / 4) + 1023) / 1024;
