@@ -232,7 +232,7 @@ svt_status svt_rope_append(const void* latent_bf16, int64_t latent_stride, const
 }
 
 size_t svt_sparse_mla_backward_workspace_size(int32_t T, int32_t H, int32_t K, int64_t num_slots) {
-  if (T < 0 || H < 0 || K < 0 || num_slots < 0) return svt::kStatusBytes;
+  if (T < 0 || H < 0 || H > 128 || K < 0 || K > (1 << 30) || num_slots < 0) return svt::kStatusBytes;  // refused
   svt::BackwardParams p{};
   p.T = T;
   p.H = H;

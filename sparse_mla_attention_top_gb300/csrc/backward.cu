@@ -21,13 +21,16 @@
 //
 // Warps: 8 softmax (S^T, dP^T -> P, dS; two of the five dKV^T blocks -> additions; dq out), 8 scatter
 // (the other blocks -> additions), 3 gather (cp.async, rows zero-filled where there is none), 1 that
-// issues the MMAs. q and dout (136 KB) and one 72 KB tile of rows fill shared memory, so the next
-// tile is gathered while step 3 runs.
+// issues the MMAs. q and dout of 64 heads (136 KB) and one 72 KB tile of rows fill shared memory, so the
+// next tile is gathered while step 3 runs. Calls of at most 32 heads keep q and dout in half of that and
+// two tiles of rows (Lay<32>).
 //
-// What bounds it: a tile takes about 4.9 us (9300 cycles). The chain product 1 (2200 cycles) -> softmax
+// What bounds it: of 64 heads, a tile takes about 4.9 us (9300 cycles). The chain product 1 (2200 cycles) -> softmax
 // (1500) -> product 2 (900) -> product 3 (2300) is 7800 with the additions left out, and the additions
 // alone, 147 KB a tile, 7200 at the 6 TB/s that the L2 takes; they meet in the few buffers between.
 // 1024 queries x 64 heads x 2048 entries: 1.07 ms (1.02 in this kernel), 690 TFLOP/s, 4.8 GB of additions.
+// Of 32 heads or fewer, a tile takes 4.3 us: the additions beside the reads of the rows (4.2 us at the
+// measured 5.4 TB/s); 333 x 16 x 2048: 338 us, with the schedule of 64 heads 369.
 #include <math_constants.h>
 
 #include <cstdint>
@@ -616,7 +619,7 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
 template <int R>
 __device__ __forceinline__ void scatter_role(const BackwardParams& p, Misc* misc, uint32_t tmem, uint32_t bars,
                                              const WaitCtl& wc) {
-  const int warp = (threadIdx.x >> 5) - kScatWarp0, lane = threadIdx.x & 31;
+  const int warp = (threadIdx.x >> 5) - kScatWarp0;
   const int quad = warp & 3;
   const int group = warp >> 2;  // takes blocks 1 and 4, or 2
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
@@ -697,9 +700,8 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const BackwardPar
 }
 
 // The first T * chunks CTAs: 2048 entries of a query's list as cache rows, and how far the live ones
-// reach. The next delta_ctas,
-// 32 heads of any queries each: (lse, delta); a head without a live entry (lse = -inf)
-// gets +inf, so that P = 0. The others zero the cache rows' sums.
+// reach. The next delta_ctas, 32 heads of any queries each: (lse, delta); a head without a live entry
+// (lse = -inf) gets +inf, so that P = 0. The others zero the cache rows' sums.
 constexpr int kPrepThreads = 256;
 constexpr int kPrepHeads = 32;
 constexpr int kListChunk = 2048;
@@ -869,6 +871,8 @@ cudaError_t launch_backward(const BackwardParams& p, const ListParams& l, cudaSt
     if (e != cudaSuccess) return e;
   }
   if (!any) return cudaMemsetAsync(p.dkv, 0, static_cast<size_t>(p.num_slots) * kRow * sizeof(uint16_t), stream);
+  // the two schedules, us for 32 and for 64 heads a row-set: 333 x 32 x 2048 355 and 381, 1024 x 16 x 2048 934 and
+  // 1015, 512 x 8 x 512 147 and 161, 64 x 32 x 200 38 and 41. More heads in sets of 32 would add every row twice
   const bool packed = p.H <= 32;
   const auto kernel = packed ? backward_kernel<32> : backward_kernel<64>;
   const uint32_t smem = packed ? kSmem<32> : kSmem<64>;

@@ -386,8 +386,8 @@ __device__ __forceinline__ void tmem_ld_16x64b_x16(uint32_t taddr, uint32_t (&r)
       : "memory");
 }
 
-// 16 lanes x 32 columns with the .16x256b shape: thread t gets lane t >> 2 (r[4 k], r[4 k + 1]) and
-// lane 8 + (t >> 2) (r[4 k + 2], r[4 k + 3]), columns 8 k + 2 (t & 3) and the next, k < 4.
+// 16 lanes x 32 or 16 columns with the .16x256b shape: thread t gets lane t >> 2 (r[4 k], r[4 k + 1]) and
+// lane 8 + (t >> 2) (r[4 k + 2], r[4 k + 3]), columns 8 k + 2 (t & 3) and the next, k < 4 or 2.
 __device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
@@ -477,6 +477,8 @@ __host__ __device__ constexpr uint32_t idesc_f32acc(int M, int N, int a_mn, int 
 // The same descriptor for the 64-byte swizzle (rows of 64 bytes; every 8 rows form a 512-byte
 // atom whose 16-byte chunks are XOR-permuted by (row / 2) % 4; layout 4 in bits 61-63).
 //   K-major operand (rows of 32 K-elements): SBO = distance between 8-row groups; LBO unused.
+//   MN-major operand (rows of 32 MN-elements): LBO = distance between its 32-element groups, SBO = between
+//   groups of 8 K.
 __device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t start, uint32_t lbo, uint32_t sbo) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((start >> 4) & 0x3FFFu);

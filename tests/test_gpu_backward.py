@@ -85,6 +85,19 @@ def test_backward_more_queries_than_sms(S, T, H, K):
     check(S, normal(1, T, H, 576), normal(2, 700, 576), lists(3, T, K, 700), normal(4, T, H, 512))
 
 
+@pytest.mark.parametrize("H", [15, 16, 17, 31, 32, 33])
+@pytest.mark.parametrize("T,K", [(1, 1), (1, 63), (3, 65), (190, 129), (37, 1100)])
+def test_backward_around_32_heads(S, T, H, K):
+    """Row-sets of 32 and of 64 heads: lists of one tile and of many, cut between CTAs and whole, dead tiles."""
+    slots = lists(102, T, K, 1200)
+    if T > 2:
+        slots[1] = -1
+        slots[2, : K // 2] = -1
+    dq, dkv, w = check(S, normal(103, T, H, 576), normal(104, 1200, 576), slots, normal(105, T, H, 512))
+    if T > 2:
+        assert not dq[1].any() and not w[1].any()
+
+
 @pytest.mark.parametrize("T,H,K,live", [(1, 4, 9000, 9000), (2, 16, 5000, 2049), (3, 1, 4097, 1), (2, 70, 4096, 0)])
 def test_backward_lists_of_several_pieces(S, T, H, K, live):
     """Long lists, their live entries ending in any piece of them (or missing, or only at the very end)."""
