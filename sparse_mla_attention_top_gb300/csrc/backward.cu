@@ -190,7 +190,7 @@ __device__ __forceinline__ void gather_role(const BackwardParams& p, uint8_t* sm
   while (it.next(s)) {
     if (s.j0 >= s.j1) continue;
     // the last segment's products are done: q and dout may be replaced
-    if (segs > 0) mbar_wait(bar(kBarSeg), (segs - 1) & 1, wc);
+    if (segs > 0 && !mbar_wait(bar(kBarSeg), (segs - 1) & 1, wc)) return;
     for (int r = r0; r < R; r += kFillStep) {
       const uint32_t ok = r < s.nvalid ? 16u : 0u;
       const uint16_t* q = p.q + (s.base + (ok ? r : 0)) * kRow + c * 8;
@@ -218,7 +218,10 @@ __device__ __forceinline__ void gather_role(const BackwardParams& p, uint8_t* sm
     for (int j = s.j0; j < s.j1; ++j, ++g) {
       constexpr uint32_t kBufs = Lay<R>::kKvBufs;
       const uint32_t buf = g % kBufs;
-      if (g >= kBufs) mbar_wait(bar(kBarKvFree + static_cast<int>(buf)), (g / kBufs - 1) & 1, wc);
+      if (g >= kBufs && !mbar_wait(bar(kBarKvFree + static_cast<int>(buf)), (g / kBufs - 1) & 1, wc)) {
+        cp_async_wait_all();  // none in flight when the CTA ends
+        return;
+      }
 #pragma unroll
       for (int i = 0; i < kFillRows; ++i) {
         const int r = r0 + kFillStep * i;
@@ -462,12 +465,15 @@ __device__ __forceinline__ void add_rows(float* dst, const int* slots, const uin
   }
 }
 
+// After the first wait that gives up, this role and scatter_role end: a barrier still in its first phase
+// answers the waits of the next tile as if it had completed, and what they guard was never written.
 template <int R>
 __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* smem, Misc* misc, uint32_t tmem,
                                              uint32_t bars, const WaitCtl& wc) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3, half = warp >> 2;
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
+  auto wait = [&](int i, uint32_t parity) -> bool { return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, wc)); };
   // S^T and dP^T (64 entries in lanes 0-15 of each quadrant): this thread's entries e and e + 8, and
   // their heads kHeads half + 8 k + 2 (lane & 3) and the next, k < kOcts
   constexpr int kHeads = R / 2, kOcts = kHeads / 8;
@@ -511,7 +517,7 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
       }
     };
     for (int j = s.j0; j < s.j1; ++j, ++g) {
-      mbar_wait(bar(kBarS), g & 1, wc);
+      if (!wait(kBarS, g & 1)) return;
       tc_fence_after();
       uint32_t sv[4 * kOcts], dv[4 * kOcts];
       tmem_ld_16x256b(lanes + Lay<R>::kTmS + kHeads * half, sv);
@@ -539,7 +545,7 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
           pd[2 * k + h] = pack_bf16x2(d[0], d[1]);
         }
       // the last tile's products with P and dS are done
-      if (g > 0) mbar_wait(bar(kBarPFree), (g - 1) & 1, wc);
+      if (g > 0 && !wait(kBarPFree, (g - 1) & 1)) return;
       if constexpr (R == 64) {
         const uint32_t at8 = at0 + 8 * 128;
         stmatrix_x4(at0 + kOffP<R>, pp[0], pp[2], pp[4], pp[6]);
@@ -567,7 +573,7 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
       // entries each
 #pragma unroll 1
       for (int cb = 0; cb < 4; cb += 3) {
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarBlock + cb), g & 1, wc))) break;
+        if (!wait(kBarBlock + cb, g & 1)) return;
         if (cb == 0 && p.weights != nullptr) put_weight(j);
         tc_fence_after();
         uint32_t v[32];
@@ -580,7 +586,7 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
     }
     // dq^T: lane = channel, this warp's heads kHeads half and on
     if (any) {
-      mbar_wait(bar(kBarDq), segs & 1, wc);
+      if (!wait(kBarDq, segs & 1)) return;
       tc_fence_after();
     }
 #pragma unroll 1
@@ -672,6 +678,8 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const BackwardPar
     misc->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // no row before the gather names one
+  if (threadIdx.x < 4 * kEntries) misc->slot[threadIdx.x / kEntries][threadIdx.x % kEntries] = -1;
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&misc->tmem), 512);
     tmem_relinquish();

@@ -392,3 +392,37 @@ def test_backward_wait_that_runs_out_is_reported_and_the_next_call_is_clean(S):
     got = S.sparse_mla_backward(*args, return_weights=True, ws=ws)
     assert ws.read_status() == 0
     assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+
+
+@pytest.mark.parametrize("T,H,K", [(40, 16, 700), (300, 32, 130), (40, 64, 700), (170, 128, 200)])
+def test_backward_wait_that_runs_out_with_several_tiles_a_cta(S, T, H, K):
+    """A CTA whose first wait gave up has tiles left to walk: it adds to no row that no list names, and writes
+    nothing outside its outputs and its part of the workspace."""
+    n, listed = 900, 800
+    kv = S.KVCache(normal(110, n, 576).cuda(), n, 1, W.KV_BF16)
+    q, dout, slots = normal(111, T, H, 576).cuda(), normal(112, T, H, 512).cuda(), lists(113, T, K, listed).cuda()
+    out, lse = forward(S, q, kv, slots)
+    need = S.svt.lib().svt_sparse_mla_backward_workspace_size(T, H, K, n)
+    ws = S.Workspace(nbytes=need + (1 << 20))
+    ws.buf[need:] = 90
+    wide_q = torch.full((T + 2, H, 576), 3.0, dtype=torch.bfloat16, device="cuda")
+    wide_kv = torch.full((n + 2, 576), 3.0, dtype=torch.bfloat16, device="cuda")
+    run = lambda: S.sparse_mla_backward(  # noqa: E731
+        q, kv, slots, SCALE, out, lse, dout, dq=wide_q[1:-1], dkv=wide_kv[1:-1], return_weights=True, ws=ws)
+    want = [x.clone() for x in run()]
+    assert ws.read_status() == 0
+    S.debug_pipeline_fault(1, 2_000_000)
+    try:
+        _, dkv, _ = run()
+        assert ws.read_status() == S.svt.DEV_ERR_TIMEOUT
+    finally:
+        S.debug_pipeline_fault()
+    assert not dkv[listed:].any()
+    for wide in (wide_q, wide_kv):
+        assert bool((wide[0] == 3).all()) and bool((wide[-1] == 3).all())
+    assert bool((ws.buf[need:] == 90).all())
+    got = run()
+    assert ws.read_status() == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+    ref, bound = R.backward(q.cpu(), kv.data.cpu(), slots.cpu().long(), SCALE, out.cpu(), lse.cpu(), dout.cpu())
+    R.within(got[1], ref[1], bound[1])
