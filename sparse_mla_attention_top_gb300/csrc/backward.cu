@@ -465,15 +465,17 @@ __device__ __forceinline__ void add_rows(float* dst, const int* slots, const uin
   }
 }
 
-// After the first wait that gives up, this role and scatter_role end: a barrier still in its first phase
-// answers the waits of the next tile as if it had completed, and what they guard was never written.
+// This role and scatter_role end at the first block of dKV^T whose wait gives up: a barrier that stays in its
+// phase answers the next tile's parity as if it had completed, for a block that was never written and rows
+// that the gather never named. The other waits may give up: what follows them stays in this CTA and the
+// call's outputs. (The loops are left by their variables: a return at this place, or one at every wait,
+// makes 333 x 16 x 2048 take 345 us instead of 338.)
 template <int R>
 __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* smem, Misc* misc, uint32_t tmem,
                                              uint32_t bars, const WaitCtl& wc) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3, half = warp >> 2;
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
-  auto wait = [&](int i, uint32_t parity) -> bool { return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, wc)); };
   // S^T and dP^T (64 entries in lanes 0-15 of each quadrant): this thread's entries e and e + 8, and
   // their heads kHeads half + 8 k + 2 (lane & 3) and the next, k < kOcts
   constexpr int kHeads = R / 2, kOcts = kHeads / 8;
@@ -517,7 +519,7 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
       }
     };
     for (int j = s.j0; j < s.j1; ++j, ++g) {
-      if (!wait(kBarS, g & 1)) return;
+      mbar_wait(bar(kBarS), g & 1, wc);
       tc_fence_after();
       uint32_t sv[4 * kOcts], dv[4 * kOcts];
       tmem_ld_16x256b(lanes + Lay<R>::kTmS + kHeads * half, sv);
@@ -545,7 +547,7 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
           pd[2 * k + h] = pack_bf16x2(d[0], d[1]);
         }
       // the last tile's products with P and dS are done
-      if (g > 0 && !wait(kBarPFree, (g - 1) & 1)) return;
+      if (g > 0) mbar_wait(bar(kBarPFree), (g - 1) & 1, wc);
       if constexpr (R == 64) {
         const uint32_t at8 = at0 + 8 * 128;
         stmatrix_x4(at0 + kOffP<R>, pp[0], pp[2], pp[4], pp[6]);
@@ -573,7 +575,11 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
       // entries each
 #pragma unroll 1
       for (int cb = 0; cb < 4; cb += 3) {
-        if (!wait(kBarBlock + cb, g & 1)) return;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarBlock + cb), g & 1, wc))) {
+          j = s.j1;  // no further tile
+          it.pos = it.hi;
+          break;
+        }
         if (cb == 0 && p.weights != nullptr) put_weight(j);
         tc_fence_after();
         uint32_t v[32];
@@ -586,7 +592,7 @@ __device__ __forceinline__ void softmax_role(const BackwardParams& p, uint8_t* s
     }
     // dq^T: lane = channel, this warp's heads kHeads half and on
     if (any) {
-      if (!wait(kBarDq, segs & 1)) return;
+      mbar_wait(bar(kBarDq), segs & 1, wc);
       tc_fence_after();
     }
 #pragma unroll 1
