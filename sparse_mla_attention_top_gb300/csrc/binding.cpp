@@ -8,6 +8,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <cuda_runtime_api.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
@@ -287,6 +288,19 @@ PyObject* distill(PyObject* const* a) {
   return t;
 }
 
+// capture_id(stream address): the id of the capture that records the stream (0 = none)
+PyObject* capture_id(PyObject* const* a) {
+  const auto stream = reinterpret_cast<cudaStream_t>(static_cast<uintptr_t>(integer(a[0])));
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo(stream, &status, &id) != cudaSuccess) {
+    (void)cudaGetLastError();
+    PyErr_SetString(PyExc_RuntimeError, "the stream's capture cannot be queried");
+    throw PyFailure{};
+  }
+  return PyLong_FromUnsignedLongLong(status == cudaStreamCaptureStatusNone ? 0 : id);
+}
+
 // Calls `f` with its arguments; no C++ exception leaves.
 template <PyObject* (*f)(PyObject* const*), int kArgs, bool kBound = true>
 PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -323,6 +337,7 @@ PyObject* bind(PyObject* const* a) {
 #define SVT_METHOD(name, f, n, bound) \
   {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<f, n, bound>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {SVT_METHOD("bind", bind, 5, false),
+                         SVT_METHOD("capture_id", capture_id, 1, false),
                          SVT_METHOD("rope", rope, 8, true),
                          SVT_METHOD("rope_append", rope_append, 15, true),
                          SVT_METHOD("sparse_mla_backward", backward, 20, true),

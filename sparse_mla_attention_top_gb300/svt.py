@@ -9,6 +9,7 @@ is no fallback. The names follow the C entry points in include/svt.h.
 from __future__ import annotations
 
 import ctypes
+import threading
 from dataclasses import dataclass
 from pathlib import Path
 from typing import Optional
@@ -167,20 +168,23 @@ class Workspace:
     """Caller-owned scratch for one stream: a 256-byte status header plus per-call space.
     Grows on demand (allocation happens here, in torch, never inside the library). Outgrown buffers
     are kept: a captured graph goes on using the one it was captured with (its status bits stay there),
-    so size a workspace before the capture where they are to be read."""
+    so size a workspace before the capture where they are to be read. A call holds `lock` while it sizes
+    the workspace and enqueues its kernels, so that threads can share one on their common stream."""
 
     def __init__(self, device=None, nbytes: int = 256):
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         self.buf = torch.zeros(max(256, nbytes), dtype=torch.uint8, device=self.device)
         self._outgrown = []
+        self.lock = threading.RLock()
 
     def ensure(self, nbytes: int) -> "Workspace":
-        if nbytes > self.buf.numel():
-            old = self.buf
-            nbytes = max(nbytes, old.numel() * 3 // 2)  # so that those kept add up to twice the last
-            self._outgrown.append(old)
-            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
-            self.buf[:256].copy_(old[:256])  # keep pending status bits
+        with self.lock:
+            if nbytes > self.buf.numel():
+                old = self.buf
+                nbytes = max(nbytes, old.numel() * 3 // 2)  # so that those kept add up to twice the last
+                self._outgrown.append(old)
+                self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+                self.buf[:256].copy_(old[:256])  # keep pending status bits
         return self
 
     @property
@@ -197,14 +201,32 @@ class Workspace:
         return int(out.value)
 
 
-_default_ws = {}
+_default_ws = {}   # (device, stream) -> Workspace
+_captured_ws = {}  # (device, stream) -> (id of its last capture, Workspace)
+_default_lock = threading.Lock()
 
 
 def default_workspace() -> Workspace:
+    """The workspace of calls that are given none: one for each stream of each device, as calls on two
+    streams may overlap. While the stream is being captured it is one of that capture's own, as two graphs
+    may be replayed at once: it lies in the graph's memory, and each replay begins by clearing its status.
+    Give captured calls a workspace where their status is to be read."""
     dev = torch.cuda.current_device()
-    ws = _default_ws.get(dev)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch.cuda.is_current_stream_capturing():
+        capture = _binding().capture_id(stream)
+        with _default_lock:
+            last, ws = _captured_ws.get((dev, stream), (None, None))
+            if last != capture:
+                ws = Workspace()
+                _captured_ws[dev, stream] = capture, ws
+        return ws
+    ws = _default_ws.get((dev, stream))
     if ws is None:
-        ws = _default_ws[dev] = Workspace()
+        with _default_lock:
+            ws = _default_ws.get((dev, stream))
+            if ws is None:
+                ws = _default_ws[dev, stream] = Workspace()
     return ws
 
 
@@ -215,12 +237,14 @@ def resolve_topk_slots(topk_pos, *, block_table=None, seq_lens=None, req_of_toke
     T, K = topk_pos.shape
     bt = _i32(block_table, "block_table")
     out = torch.empty((T, K), dtype=torch.int32, device=topk_pos.device) if out is None else out
-    ws = (ws or default_workspace()).ensure(lib().svt_resolve_workspace_size())
-    _check(lib().svt_resolve_topk_slots(_ptr(topk_pos), T, K, _ptr(_i32(topk_len, "topk_len")),
-                                        _ptr(_i32(req_of_token, "req_of_token")), _ptr(bt),
-                                        0 if bt is None else bt.shape[0], 0 if bt is None else bt.shape[1],
-                                        _ptr(_i32(seq_lens, "seq_lens")), int(page_size), int(num_pages), _ptr(out),
-                                        ws.ptr, ws.nbytes, _stream()), "svt_resolve_topk_slots")
+    ws = ws or default_workspace()
+    with ws.lock:
+        ws.ensure(lib().svt_resolve_workspace_size())
+        _check(lib().svt_resolve_topk_slots(_ptr(topk_pos), T, K, _ptr(_i32(topk_len, "topk_len")),
+                                            _ptr(_i32(req_of_token, "req_of_token")), _ptr(bt),
+                                            0 if bt is None else bt.shape[0], 0 if bt is None else bt.shape[1],
+                                            _ptr(_i32(seq_lens, "seq_lens")), int(page_size), int(num_pages), _ptr(out),
+                                            ws.ptr, ws.nbytes, _stream()), "svt_resolve_topk_slots")
     return out
 
 
@@ -239,13 +263,15 @@ def sparse_mla_decode(q, kv: KVCache, topk, softmax_scale: float, *, block_table
         out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=q.device)
     if lse is None and return_lse:
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    ws = (ws or default_workspace()).ensure(lib().svt_sparse_mla_decode_workspace_size(T, H, K, num_splits))
+    ws = ws or default_workspace()
     kvc = kv._c()
-    _check(lib().svt_sparse_mla_decode(_ptr(q), T, H, ctypes.byref(kvc), _ptr(bt), 0 if bt is None else bt.shape[0],
-                                       0 if bt is None else bt.shape[1], _ptr(_i32(req_of_token, "req_of_token")),
-                                       _ptr(_i32(seq_lens, "seq_lens")), _ptr(topk), K,
-                                       _ptr(_i32(topk_len, "topk_len")), float(softmax_scale), _ptr(out), _ptr(lse),
-                                       int(num_splits), ws.ptr, ws.nbytes, _stream()), "svt_sparse_mla_decode")
+    with ws.lock:
+        ws.ensure(lib().svt_sparse_mla_decode_workspace_size(T, H, K, num_splits))
+        _check(lib().svt_sparse_mla_decode(_ptr(q), T, H, ctypes.byref(kvc), _ptr(bt), 0 if bt is None else bt.shape[0],
+                                           0 if bt is None else bt.shape[1], _ptr(_i32(req_of_token, "req_of_token")),
+                                           _ptr(_i32(seq_lens, "seq_lens")), _ptr(topk), K,
+                                           _ptr(_i32(topk_len, "topk_len")), float(softmax_scale), _ptr(out), _ptr(lse),
+                                           int(num_splits), ws.ptr, ws.nbytes, _stream()), "svt_sparse_mla_decode")
     return out, lse
 
 
@@ -259,9 +285,11 @@ def build_group_union(slots, G: int, num_slots: int, *, topk_len=None, enc=None,
         enc = torch.empty((groups, G * K), dtype=torch.int32, device=slots.device)
     if lens is None:
         lens = torch.empty((groups,), dtype=torch.int32, device=slots.device)
-    ws = (ws or default_workspace()).ensure(lib().svt_build_group_union_workspace_size(T, K, G))
-    _check(lib().svt_build_group_union(_ptr(slots), _ptr(_i32(topk_len, "topk_len")), T, K, int(G), int(num_slots),
-                                       _ptr(enc), _ptr(lens), ws.ptr, ws.nbytes, _stream()), "svt_build_group_union")
+    ws = ws or default_workspace()
+    with ws.lock:
+        ws.ensure(lib().svt_build_group_union_workspace_size(T, K, G))
+        _check(lib().svt_build_group_union(_ptr(slots), _ptr(_i32(topk_len, "topk_len")), T, K, int(G), int(num_slots),
+                                           _ptr(enc), _ptr(lens), ws.ptr, ws.nbytes, _stream()), "svt_build_group_union")
     return enc, lens
 
 
@@ -277,12 +305,14 @@ def sparse_mla_prefill_grouped(q, G: int, kv: KVCache, enc, lens, K: int, softma
         out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=q.device)
     if lse is None and return_lse:
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    ws = (ws or default_workspace()).ensure(lib().svt_sparse_mla_prefill_grouped_workspace_size(T, H, G))
+    ws = ws or default_workspace()
     kvc = kv._c()
     name = "svt_sparse_mla_prefill_grouped_union_tile" if union_tile else "svt_sparse_mla_prefill_grouped"
-    _check(getattr(lib(), name)(_ptr(q), T, H, int(G), ctypes.byref(kvc), _ptr(_i32(enc, "enc")),
-                                _ptr(_i32(lens, "lens")), int(K), float(softmax_scale), _ptr(out), _ptr(lse), ws.ptr,
-                                ws.nbytes, _stream()), name)
+    with ws.lock:
+        ws.ensure(lib().svt_sparse_mla_prefill_grouped_workspace_size(T, H, G))
+        _check(getattr(lib(), name)(_ptr(q), T, H, int(G), ctypes.byref(kvc), _ptr(_i32(enc, "enc")),
+                                    _ptr(_i32(lens, "lens")), int(K), float(softmax_scale), _ptr(out), _ptr(lse), ws.ptr,
+                                    ws.nbytes, _stream()), name)
     return out, lse
 
 
@@ -376,9 +406,10 @@ def rope_append(latent, k_rope, positions, slots, kv: KVCache, freqs, *, layout:
     queries' rope columns into q_out (a new tensor when None; q[..., 512:] of a [T, H, 576] q fits)
     in the same launch. Returns q_out."""
     ws = ws or default_workspace()
-    r = (_fast or _binding()).rope_append(latent, k_rope, positions, slots, kv.data, kv.num_pages, kv.page_size,
-                                          kv.row_stride_bytes, kv.dtype, freqs, _choice(layout, ROPE_LAYOUTS, "layout"),
-                                          amplitude, q_rope, q_out, ws.buf)
+    with ws.lock:
+        r = (_fast or _binding()).rope_append(latent, k_rope, positions, slots, kv.data, kv.num_pages, kv.page_size,
+                                              kv.row_stride_bytes, kv.dtype, freqs, _choice(layout, ROPE_LAYOUTS, "layout"),
+                                              amplitude, q_rope, q_out, ws.buf)
     if type(r) is int:
         _check(r, "svt_rope_append")
     return r
@@ -391,15 +422,16 @@ def sparse_mla_backward(q, kv: KVCache, topk, softmax_scale: float, out, lse, do
     query's own list). out and lse are the forward's; dout (and dlse) their gradients. Returns
     (dq [T, H, 576] bf16, dkv [num_slots, 576] bf16, weights [T, K] fp32 or None)."""
     ws = ws or default_workspace()
-    for _ in range(2):
-        r = (_fast or _binding()).sparse_mla_backward(
-            q, kv.data, kv.num_pages, kv.page_size, kv.row_stride_bytes, kv.dtype, topk, softmax_scale, out, lse, dout, dlse,
-            block_table, seq_lens, req_of_token, topk_len, dq, dkv, return_weights, ws.buf)
-        if type(r) is not int:
-            return r
-        if r >= 0:
-            break
-        ws.ensure(-r)
+    with ws.lock:
+        for _ in range(2):
+            r = (_fast or _binding()).sparse_mla_backward(
+                q, kv.data, kv.num_pages, kv.page_size, kv.row_stride_bytes, kv.dtype, topk, softmax_scale, out, lse, dout,
+                dlse, block_table, seq_lens, req_of_token, topk_len, dq, dkv, return_weights, ws.buf)
+            if type(r) is not int:
+                return r
+            if r >= 0:
+                break
+            ws.ensure(-r)
     _check(r, "svt_sparse_mla_backward")
 
 

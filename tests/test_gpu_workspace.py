@@ -1,0 +1,112 @@
+"""Workspaces: calls that are given none, on streams, in threads and in graphs at once."""
+
+import threading
+
+import pytest
+import torch
+
+from sparse_mla_attention_top_gb300 import workloads as W
+from tests import _layer_ref as R
+
+pytestmark = pytest.mark.gpu
+SCALE = 576 ** -0.5
+
+
+@pytest.fixture(scope="module")
+def S():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import sparse_mla_attention_top_gb300 as S
+    from sparse_mla_attention_top_gb300 import build
+
+    build.build()
+    return S
+
+
+class Step:
+    """A split decode and its backward pass on inputs of a seed, with the results of calls made one by one."""
+
+    def __init__(self, S, seed, T=24, H=64, K=300, n=500):
+        g = torch.Generator().manual_seed(seed)
+        normal = lambda *s: torch.randn(s, generator=g).to(torch.bfloat16)  # noqa: E731
+        self.S = S
+        self.kv = S.KVCache(normal(n, 576).cuda(), n, 1, W.KV_BF16)
+        self.q, self.dout = normal(T, H, 576).cuda(), normal(T, H, 512).cuda()
+        self.topk = torch.stack([torch.randperm(n, generator=g)[:K] for _ in range(T)]).to(torch.int32).cuda()
+        self.want = self.run(S.Workspace())
+        torch.cuda.synchronize()
+        cpu = lambda t: t.cpu()  # noqa: E731
+        self.ref, self.bound = R.backward(cpu(self.q), cpu(self.kv.data), cpu(self.topk).long(), SCALE, cpu(self.want[0]),
+                                          cpu(self.want[1]), cpu(self.dout))
+
+    def run(self, ws=None):
+        out, lse = self.S.sparse_mla_decode(self.q, self.kv, self.topk, SCALE, num_splits=3, ws=ws)
+        return out, lse, *self.S.sparse_mla_backward(self.q, self.kv, self.topk, SCALE, out, lse, self.dout,
+                                                     return_weights=True, ws=ws)
+
+    def check(self, got):
+        for i in (0, 1, 2, 4):  # all but the cache rows' sums repeat exactly
+            assert torch.equal(got[i], self.want[i]), i
+        R.within(got[3], self.ref[1], self.bound[1])
+
+
+def test_default_workspaces_on_two_streams_at_once(S):
+    steps = [Step(S, 1), Step(S, 2, T=30, H=16, K=200)]
+    streams = [torch.cuda.Stream() for _ in steps]
+    got = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for step, stream, out in zip(steps, streams, got):
+            with torch.cuda.stream(stream):
+                out.append(step.run())
+    torch.cuda.synchronize()
+    for step, stream, out in zip(steps, streams, got):
+        for x in out:
+            step.check(x)
+        with torch.cuda.stream(stream):
+            assert S.svt.default_workspace().read_status() == 0
+
+
+def test_default_workspace_of_threads_on_one_stream(S):
+    steps = [Step(S, 3), Step(S, 4, T=30, H=16, K=200), Step(S, 5, T=7, H=128, K=400)]
+    got, errors = [[] for _ in steps], []
+
+    def loop(step, out):
+        try:
+            for _ in range(8):
+                out.append(step.run())
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=loop, args=a) for a in zip(steps, got)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for step, out in zip(steps, got):
+        for x in out:
+            step.check(x)
+    assert S.svt.default_workspace().read_status() == 0
+
+
+def test_default_workspaces_of_graphs_replayed_at_once(S):
+    """Captured by the same stream, as torch.cuda.graph does; the second graph is the larger one."""
+    steps = [Step(S, 6), Step(S, 7, T=60, H=64, K=400)]
+    graphs, got = [], []
+    for step in steps:
+        step.run()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(step.run())
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in steps]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for g, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                g.replay()
+        steps[0].run()  # beside them, on the current stream
+    torch.cuda.synchronize()
+    for step, x in zip(steps, got):
+        step.check(x)

@@ -4,6 +4,7 @@ reaches a device)."""
 
 import ctypes
 import math
+import threading
 
 import pytest
 import torch
@@ -192,3 +193,46 @@ def test_the_binding_refuses_what_is_no_tensor(L):
         svt._binding().rope(torch.zeros(1, 1, 2))
     with pytest.raises(ValueError):
         S.rope(torch.zeros(1, 1, 2), torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.float64), layout="x")
+
+
+def test_default_workspaces_are_one_a_stream_and_one_a_capture(monkeypatch):
+    """A workspace is scratch for one stream: calls on two streams, or in two graphs, may overlap."""
+    at = dict(device=0, stream=0, capture=0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: at["device"])
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: at["stream"], raising=False)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: at["capture"] != 0)
+    monkeypatch.setattr(svt, "_binding", lambda: type("B", (), {"capture_id": staticmethod(lambda s: at["capture"])}))
+    made = svt.Workspace
+    monkeypatch.setattr(svt, "Workspace", lambda: made("cpu"))
+    monkeypatch.setattr(svt, "_default_ws", {})
+    monkeypatch.setattr(svt, "_captured_ws", {}, raising=False)
+
+    def ws(**kw):
+        at.update(device=0, stream=0, capture=0)
+        at.update(kw)
+        return svt.default_workspace()
+    plain = ws()
+    assert ws() is plain and ws(stream=7) is ws(stream=7)
+    recorded = ws(stream=7, capture=3)
+    assert ws(stream=7, capture=3) is recorded
+    others = [plain, ws(stream=7), ws(device=1), recorded, ws(stream=8, capture=3), ws(stream=7, capture=4)]
+    assert len({id(w) for w in others}) == len(others)
+
+
+def test_threads_share_a_growing_workspace(monkeypatch):
+    """A call sees the address and the size of one buffer, whatever other threads ask for meanwhile."""
+    ws = svt.Workspace("cpu")
+    seen, stop = [], threading.Event()
+
+    def grow():
+        for n in range(1000, 200_000, 1000):
+            ws.ensure(n)
+        stop.set()
+    t = threading.Thread(target=grow)
+    t.start()
+    while not stop.is_set():
+        with ws.lock:
+            p, n = ws.buf.data_ptr(), ws.nbytes
+            seen.append(p == ws.ptr.value and n == ws.buf.numel())
+    t.join()
+    assert all(seen) and ws.nbytes >= 199_000
