@@ -166,25 +166,33 @@ class KVCache:
 
 class Workspace:
     """Caller-owned scratch for one stream: a 256-byte status header plus per-call space.
-    Grows on demand (allocation happens here, in torch, never inside the library). Outgrown buffers
-    are kept: a captured graph goes on using the one it was captured with (its status bits stay there),
-    so size a workspace before the capture where they are to be read. A call holds `lock` while it sizes
-    the workspace and enqueues its kernels, so that threads can share one on their common stream."""
+    Grows on demand, to the size asked for (allocation happens here, in torch, never inside the library).
+    An outgrown buffer goes back to torch, unless a call that used it was captured: the graph goes on using
+    it, so it is kept, and its status is read with the workspace's. A call holds `lock` while it sizes the
+    workspace and enqueues its kernels, so that threads can share one on their common stream."""
 
     def __init__(self, device=None, nbytes: int = 256):
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         self.buf = torch.zeros(max(256, nbytes), dtype=torch.uint8, device=self.device)
-        self._outgrown = []
+        self._captured = False  # whether a captured call uses buf
+        self._kept = []
         self.lock = threading.RLock()
 
     def ensure(self, nbytes: int) -> "Workspace":
+        """At least nbytes. Every call makes this one, under the lock, before it takes ptr and nbytes."""
         with self.lock:
+            capturing = self.buf.is_cuda and torch.cuda.is_current_stream_capturing()
             if nbytes > self.buf.numel():
                 old = self.buf
-                nbytes = max(nbytes, old.numel() * 3 // 2)  # so that those kept add up to twice the last
-                self._outgrown.append(old)
                 self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
-                self.buf[:256].copy_(old[:256])  # keep pending status bits
+                if self._captured or capturing:
+                    self._kept.append(old)
+                else:
+                    self.buf[:256].copy_(old[:256])  # keep pending status bits
+                    if old.is_cuda:
+                        old.record_stream(torch.cuda.current_stream())  # earlier calls may still run
+                self._captured = False
+            self._captured |= capturing
         return self
 
     @property
@@ -196,9 +204,12 @@ class Workspace:
         return self.buf.numel()
 
     def read_status(self, stream=None) -> int:
-        out = ctypes.c_int32(0)
-        _check(lib().svt_read_status(self.ptr, _stream(stream), ctypes.byref(out)), "svt_read_status")
-        return int(out.value)
+        bits = 0
+        for buf in (self.buf, *self._kept):
+            out = ctypes.c_int32(0)
+            _check(lib().svt_read_status(_ptr(buf), _stream(stream), ctypes.byref(out)), "svt_read_status")
+            bits |= int(out.value)
+        return bits
 
 
 _default_ws = {}   # (device, stream) -> Workspace
@@ -407,6 +418,7 @@ def rope_append(latent, k_rope, positions, slots, kv: KVCache, freqs, *, layout:
     in the same launch. Returns q_out."""
     ws = ws or default_workspace()
     with ws.lock:
+        ws.ensure(256)
         r = (_fast or _binding()).rope_append(latent, k_rope, positions, slots, kv.data, kv.num_pages, kv.page_size,
                                               kv.row_stride_bytes, kv.dtype, freqs, _choice(layout, ROPE_LAYOUTS, "layout"),
                                               amplitude, q_rope, q_out, ws.buf)
@@ -423,6 +435,7 @@ def sparse_mla_backward(q, kv: KVCache, topk, softmax_scale: float, out, lse, do
     (dq [T, H, 576] bf16, dkv [num_slots, 576] bf16, weights [T, K] fp32 or None)."""
     ws = ws or default_workspace()
     with ws.lock:
+        ws.ensure(256)
         for _ in range(2):
             r = (_fast or _binding()).sparse_mla_backward(
                 q, kv.data, kv.num_pages, kv.page_size, kv.row_stride_bytes, kv.dtype, topk, softmax_scale, out, lse, dout,
@@ -464,8 +477,10 @@ def gather_probe(kv: KVCache, slots, mode: int = 0, *, out=None, ws: Optional[Wo
         out = torch.empty((n,), dtype=torch.int32, device=slots.device)
     ws = default_workspace() if ws is None else ws
     kvc = kv._c()
-    _check(lib().svt_gather_probe(ctypes.byref(kvc), _ptr(slots), n, int(mode), _ptr(out), ws.ptr, ws.nbytes,
-                                  _stream()), "svt_gather_probe")
+    with ws.lock:
+        ws.ensure(256)
+        _check(lib().svt_gather_probe(ctypes.byref(kvc), _ptr(slots), n, int(mode), _ptr(out), ws.ptr, ws.nbytes,
+                                      _stream()), "svt_gather_probe")
     return out
 
 
@@ -481,6 +496,8 @@ def tensor_probe(k_rows, q, pt, reps: int = 1, grid: int = 1, *, ws: Optional[Wo
     o_out = torch.empty((512, 64), dtype=torch.float32, device=dev)
     cycles = torch.empty((int(grid),), dtype=torch.int64, device=dev)
     ws = default_workspace() if ws is None else ws
-    _check(lib().svt_tensor_probe(_ptr(k_rows), _ptr(q), _ptr(pt), int(reps), int(grid), _ptr(s_out), _ptr(o_out),
-                                  _ptr(cycles), ws.ptr, ws.nbytes, _stream()), "svt_tensor_probe")
+    with ws.lock:
+        ws.ensure(256)
+        _check(lib().svt_tensor_probe(_ptr(k_rows), _ptr(q), _ptr(pt), int(reps), int(grid), _ptr(s_out), _ptr(o_out),
+                                      _ptr(cycles), ws.ptr, ws.nbytes, _stream()), "svt_tensor_probe")
     return s_out, o_out, cycles

@@ -110,3 +110,31 @@ def test_default_workspaces_of_graphs_replayed_at_once(S):
     torch.cuda.synchronize()
     for step, x in zip(steps, got):
         step.check(x)
+
+
+def test_outgrown_buffers_are_kept_for_captured_calls_alone(S):
+    step = Step(S, 8)
+    ws = S.Workspace()
+    torch.cuda.synchronize()
+    for n in (1 << 20, 1 << 28, (1 << 28) + 1):
+        before = torch.cuda.memory_allocated() - ws.nbytes
+        ws.ensure(n)
+        assert ws.nbytes == n and torch.cuda.memory_allocated() - n <= before + 512
+    ws = S.Workspace()
+    step.run(ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step.run(ws)
+    used, bad = ws.buf.data_ptr(), torch.tensor([500, -1, 3], dtype=torch.int32, device="cuda")
+    ws.ensure(ws.nbytes + (1 << 20))
+    junk = [torch.full((1 << 18,), 7, device="cuda") for _ in range(16)]  # over what was freed, if it was
+    for x in got:
+        x.fill_(5)
+    g.replay()
+    step.check(got)
+    assert ws.buf.data_ptr() != used and ws.read_status() == 0
+    # what a replay reports is read with the workspace, though it lies in the buffer of the capture
+    step.topk[0, :3] = bad
+    g.replay()
+    assert ws.read_status() == S.svt.DEV_ERR_INDEX_RANGE and ws.read_status() == 0
+    del junk

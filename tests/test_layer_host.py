@@ -3,8 +3,10 @@ frequencies against their formulas, and refused arguments (every refusal happens
 reaches a device)."""
 
 import ctypes
+import gc
 import math
 import threading
+import weakref
 
 import pytest
 import torch
@@ -236,3 +238,15 @@ def test_threads_share_a_growing_workspace(monkeypatch):
             seen.append(p == ws.ptr.value and n == ws.buf.numel())
     t.join()
     assert all(seen) and ws.nbytes >= 199_000
+
+
+def test_outgrown_workspace_buffers_go_back():
+    ws = svt.Workspace("cpu")
+    ws.buf[0] = 2  # a pending status bit
+    before = [weakref.ref(ws.buf)]
+    for n in (1000, 5000, 5001):
+        ws.ensure(n)
+        assert ws.nbytes == n and ws.buf[0] == 2
+        before.append(weakref.ref(ws.buf))
+    gc.collect()
+    assert [r() is None for r in before] == [True, True, True, False]
