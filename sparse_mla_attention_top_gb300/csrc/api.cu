@@ -40,6 +40,9 @@ int sm_count() {
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// Whether num_pages * page_size rows (both > 0) fit 31 bits; the product itself may not fit 64.
+bool rows_fit(long long num_pages, int page_size) { return num_pages <= ((1ll << 31) - 1) / page_size; }
+
 // Checks the cache descriptor and returns its row stride in bytes.
 svt_status check_kv(const svt_kv_cache* kv, long long* row_stride) {
   if (kv == nullptr) return fail(SVT_ERR_INVALID_ARG, "kv is null");
@@ -52,7 +55,7 @@ svt_status check_kv(const svt_kv_cache* kv, long long* row_stride) {
   const int stride = kv->row_stride_bytes == 0 ? packed : kv->row_stride_bytes;
   if (stride < packed || stride % 16 != 0)
     return fail(SVT_ERR_INVALID_ARG, "row_stride_bytes %d must be 0 or >= %d and a multiple of 16", stride, packed);
-  if (kv->num_pages * static_cast<long long>(kv->page_size) >= (1ll << 31))
+  if (!rows_fit(kv->num_pages, kv->page_size))
     return fail(SVT_ERR_UNSUPPORTED, "the cache must hold fewer than 2^31 rows");
   *row_stride = stride;
   return SVT_OK;
@@ -257,7 +260,7 @@ svt_status svt_resolve_topk_slots(const int32_t* topk_pos, int32_t T, int32_t K,
                                   int32_t* slots_out, void* ws, size_t ws_bytes, svt_stream_t stream) {
   if (T < 0 || K < 0) return fail(SVT_ERR_INVALID_ARG, "T and K must be >= 0");
   if (page_size <= 0 || num_pages <= 0) return fail(SVT_ERR_INVALID_ARG, "page_size and num_pages must be > 0");
-  if (num_pages * static_cast<long long>(page_size) >= (1ll << 31))
+  if (!rows_fit(num_pages, page_size))
     return fail(SVT_ERR_UNSUPPORTED, "the cache must hold fewer than 2^31 rows");
   if (block_table != nullptr && (num_reqs <= 0 || max_blocks <= 0))
     return fail(SVT_ERR_INVALID_ARG, "num_reqs and max_blocks must be > 0 with a block table");

@@ -250,3 +250,21 @@ def test_outgrown_workspace_buffers_go_back():
         before.append(weakref.ref(ws.buf))
     gc.collect()
     assert [r() is None for r in before] == [True, True, True, False]
+
+
+def test_page_counts_whose_rows_wrap_round_are_refused(L):
+    """2^62 pages of 4 rows are 2^64 rows, no rows in 64 bits; and the border of 2^31 rows."""
+    uns = svt.SVT_ERR_UNSUPPORTED
+    for pages, size, ok in ((1 << 62, 4, False), (1 << 32, 1 << 30, False), ((1 << 63) - 1, 2, False), (1 << 31, 1, False),
+                            (1, (1 << 31) - 1, True), ((1 << 31) - 1, 1, True), (1 << 25, 64, False), ((1 << 25) - 1, 64, True)):
+        want = svt.SVT_OK if ok else uns
+        kv = ctypes.byref(_kv(pages=pages, page_size=size))
+        assert L.svt_sparse_mla_decode(None, 0, 8, kv, None, 0, 0, None, None, None, 0, None, ctypes.c_float(1), None, None, 0,
+                                       WS, 256, None) == want
+        assert L.svt_rope_append(None, 512, None, 64, None, None, 0, kv, A, 0, ctypes.c_float(1), None, 0, 0, 0, None, 0, 0,
+                                 WS, 256, None) == want
+        # no output, and a workspace of any size: refused in any case, for its rows or for that
+        assert L.svt_sparse_mla_backward(None, 0, 8, kv, None, 0, 0, None, None, None, 0, None, ctypes.c_float(1), None, None,
+                                         None, None, None, None, None, WS, 1 << 50, None) == (svt.SVT_ERR_INVALID_ARG if ok else uns)
+        assert L.svt_resolve_topk_slots(None, 0, 0, None, None, None, 0, 0, None, size, pages, None, WS, 256, None) in (
+            (svt.SVT_OK, svt.SVT_ERR_CUDA) if ok else (uns,))
