@@ -269,8 +269,6 @@ svt_status svt_sparse_mla_backward(const void* q_bf16, int32_t T, int32_t H, con
   p.num_slots = num_slots;
   svt::plan_backward(p, sm_count());
   const BackwardWs w = backward_ws(p);
-  st = svt::check_workspace(ws, ws_bytes, w.end);
-  if (st != SVT_OK) return st;
   if (dkv_bf16 == nullptr || !aligned(dkv_bf16, 16))
     return set_last_error(SVT_ERR_INVALID_ARG, "dkv must be a 16-byte aligned array");
   if (T > 0) {
@@ -280,6 +278,9 @@ svt_status svt_sparse_mla_backward(const void* q_bf16, int32_t T, int32_t H, con
       return set_last_error(SVT_ERR_INVALID_ARG, "q, out, dout and dq must be 16-byte aligned");
     if (K > 0 && topk == nullptr) return set_last_error(SVT_ERR_INVALID_ARG, "topk must not be null");
   }
+  // the last check: a call that is refused for anything else is refused before its workspace is made
+  st = svt::check_workspace(ws, ws_bytes, w.end);
+  if (st != SVT_OK) return st;
   p.q = static_cast<const uint16_t*>(q_bf16);
   p.out = static_cast<const uint16_t*>(out_bf16);
   p.dout = static_cast<const uint16_t*>(dout_bf16);

@@ -208,7 +208,9 @@ PyObject* backward(PyObject* const* a) {
                     {dlse, "dlse"}, {bt, "block_table"}, {seq, "seq_lens"}, {req, "req_of_token"}, {len, "topk_len"},
                     {dq, "dq"}, {dkv, "dkv"}});
   const svt_kv_cache kv = cache_of(data, a + 2);
-  const int64_t n = kv.num_pages * kv.page_size;
+  // (rows that no cache has are left to the library; a product that does not fit is none of dkv's)
+  int64_t n = 0;
+  if (__builtin_mul_overflow(kv.num_pages, static_cast<int64_t>(kv.page_size), &n)) n = -1;
   const auto i32 = at::kInt, f32 = at::kFloat, bf16 = at::kBFloat16;
   const void* p_bt = shaped(bt, "block_table", i32, {reqs, blocks});
   const void* p_req = shaped(req, "req_of_token", i32, {T});
@@ -221,6 +223,20 @@ PyObject* backward(PyObject* const* a) {
   const void* p_dlse = shaped(dlse, "dlse", f32, {T, H});
   void* p_dq = shaped(dq, "dq", bf16, {T, H, 576});
   void* p_dkv = shaped(dkv, "dkv", bf16, {n, 576});
+  const float scale = real(a[7]);
+  auto call = [&](void* to_dq, void* to_dkv, float* to_weights, size_t ws_bytes) {
+    return g_backward(q.data_ptr(), int32(T), int32(H), &kv, static_cast<const int32_t*>(p_bt), int32(reqs),
+                      int32(blocks), static_cast<const int32_t*>(p_req), static_cast<const int32_t*>(p_seq),
+                      static_cast<const int32_t*>(p_topk), int32(K), static_cast<const int32_t*>(p_len), scale, p_out,
+                      static_cast<const float*>(p_lse), p_dout, static_cast<const float*>(p_dlse), to_dq, to_dkv,
+                      to_weights, ws.data_ptr(), ws_bytes, stream);
+  };
+  // A call without a workspace is refused, for that or for another reason, which comes first: only a call
+  // that the library takes makes its outputs and asks for its workspace (an aligned address stands in for
+  // the outputs).
+  void* const any = reinterpret_cast<void*>(uintptr_t{256});
+  svt_status st = call(dq ? p_dq : any, dkv ? p_dkv : any, nullptr, 0);
+  if (st != SVT_ERR_WORKSPACE) return PyLong_FromLong(st);
   const size_t need = g_backward_ws(int32(T), int32(H), int32(K), n);
   if (ws.nbytes() < need) return PyLong_FromLongLong(-static_cast<long long>(need));
   at::Tensor made_q, made_kv, weights;
@@ -229,17 +245,11 @@ PyObject* backward(PyObject* const* a) {
     p_dq = made_q.data_ptr();
   }
   if (dkv == nullptr) {
-    if (n < 0) type_error("%s must have rows", "kv data");
     made_kv = at::empty({n, 576}, q.options());
     p_dkv = made_kv.data_ptr();
   }
   if (PyObject_IsTrue(a[18])) weights = at::empty({T, K}, lse.options());
-  const svt_status st = g_backward(
-      q.data_ptr(), int32(T), int32(H), &kv, static_cast<const int32_t*>(p_bt), int32(reqs), int32(blocks),
-      static_cast<const int32_t*>(p_req), static_cast<const int32_t*>(p_seq), static_cast<const int32_t*>(p_topk),
-      int32(K), static_cast<const int32_t*>(p_len), real(a[7]), p_out, static_cast<const float*>(p_lse), p_dout,
-      static_cast<const float*>(p_dlse), p_dq, p_dkv, weights.defined() ? static_cast<float*>(weights.data_ptr()) : nullptr,
-      ws.data_ptr(), ws.nbytes(), stream);
+  st = call(p_dq, p_dkv, weights.defined() ? static_cast<float*>(weights.data_ptr()) : nullptr, ws.nbytes());
   if (st != SVT_OK) return PyLong_FromLong(st);
   PyObject* r = PyTuple_New(3);
   if (r == nullptr) return nullptr;

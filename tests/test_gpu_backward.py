@@ -426,3 +426,26 @@ def test_backward_wait_that_runs_out_with_several_tiles_a_cta(S, T, H, K):
     assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
     ref, bound = R.backward(q.cpu(), kv.data.cpu(), slots.cpu().long(), SCALE, out.cpu(), lse.cpu(), dout.cpu())
     R.within(got[1], ref[1], bound[1])
+
+
+def test_backward_refused_calls_allocate_nothing(S):
+    """The library's refusal comes before the workspace grows and before dq and dkv are made."""
+    n = 4096
+    z = lambda *s, d=torch.bfloat16: torch.zeros(s, dtype=d, device="cuda")  # noqa: E731
+    good = S.KVCache(z(n, 576), n, 1, W.KV_BF16)
+    e4m3 = S.KVCache(z(n, 656, d=torch.uint8), n, 1, W.KV_FP8_E4M3)
+    # rows that no memory holds: page counts of 2^40, and of 2^62 pages of 4 (2^64 rows wrap to none)
+    huge = S.KVCache(good.data, 1 << 40, 1, W.KV_BF16)
+    wraps = S.KVCache(good.data, 1 << 62, 4, W.KV_BF16)
+    unsupported, invalid = S.svt.SVT_ERR_UNSUPPORTED, S.svt.SVT_ERR_INVALID_ARG
+    for kv, H, kw, status in ((e4m3, 4, {}, unsupported), (good, 129, {}, unsupported), (huge, 4, {}, unsupported),
+                              (wraps, 4, {}, unsupported), (good, 4, dict(scale=math.inf), invalid)):
+        args = (z(1, H, 576), kv, z(1, 2, d=torch.int32), kw.get("scale", SCALE), z(1, H, 512), z(1, H, d=torch.float32),
+                z(1, H, 512))
+        ws = S.Workspace()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        with pytest.raises(S.SvtError) as e:
+            S.sparse_mla_backward(*args, ws=ws)
+        assert e.value.status == status
+        assert ws.nbytes == 256 and torch.cuda.max_memory_allocated() == before
