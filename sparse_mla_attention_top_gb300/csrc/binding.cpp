@@ -212,7 +212,10 @@ PyObject* backward(PyObject* const* a) {
   int64_t n = 0;
   if (__builtin_mul_overflow(kv.num_pages, static_cast<int64_t>(kv.page_size), &n)) n = -1;
   const auto i32 = at::kInt, f32 = at::kFloat, bf16 = at::kBFloat16;
+  // an aligned address in the place of a tensor that has none; it is never read or written
+  void* const any = reinterpret_cast<void*>(uintptr_t{256});
   const void* p_bt = shaped(bt, "block_table", i32, {reqs, blocks});
+  if (bt != nullptr && bt->numel() == 0 && T > 0) p_bt = any;  // refused for its sizes: null would be no table
   const void* p_req = shaped(req, "req_of_token", i32, {T});
   const void* p_seq = bt ? shaped(seq, "seq_lens", i32, {reqs}) : nullptr;
   const void* p_topk = shaped(&topk, "topk", i32, {T, K});
@@ -232,9 +235,7 @@ PyObject* backward(PyObject* const* a) {
                       to_weights, ws.data_ptr(), ws_bytes, stream);
   };
   // A call without a workspace is refused, for that or for another reason, which comes first: only a call
-  // that the library takes makes its outputs and asks for its workspace (an aligned address stands in for
-  // the outputs).
-  void* const any = reinterpret_cast<void*>(uintptr_t{256});
+  // that the library takes makes its outputs and asks for its workspace.
   svt_status st = call(dq ? p_dq : any, dkv ? p_dkv : any, nullptr, 0);
   if (st != SVT_ERR_WORKSPACE) return PyLong_FromLong(st);
   const size_t need = g_backward_ws(int32(T), int32(H), int32(K), n);

@@ -143,6 +143,12 @@ def _i32(t: Optional[torch.Tensor], name: str) -> Optional[torch.Tensor]:
     return t
 
 
+def _table(bt: Optional[torch.Tensor], T: int):
+    """The address of a block table. An empty one has none, which would read positions as slots: for queries
+    to resolve it gets an address that is never read, and the library refuses its sizes."""
+    return ctypes.c_void_p(256) if bt is not None and bt.numel() == 0 and T > 0 else _ptr(bt)
+
+
 @dataclass
 class KVCache:
     """A paged latent cache in device memory: `data` is uint8 [num_pages * page_size, row_bytes]
@@ -252,7 +258,7 @@ def resolve_topk_slots(topk_pos, *, block_table=None, seq_lens=None, req_of_toke
     with ws.lock:
         ws.ensure(lib().svt_resolve_workspace_size())
         _check(lib().svt_resolve_topk_slots(_ptr(topk_pos), T, K, _ptr(_i32(topk_len, "topk_len")),
-                                            _ptr(_i32(req_of_token, "req_of_token")), _ptr(bt),
+                                            _ptr(_i32(req_of_token, "req_of_token")), _table(bt, T),
                                             0 if bt is None else bt.shape[0], 0 if bt is None else bt.shape[1],
                                             _ptr(_i32(seq_lens, "seq_lens")), int(page_size), int(num_pages), _ptr(out),
                                             ws.ptr, ws.nbytes, _stream()), "svt_resolve_topk_slots")
@@ -278,7 +284,7 @@ def sparse_mla_decode(q, kv: KVCache, topk, softmax_scale: float, *, block_table
     kvc = kv._c()
     with ws.lock:
         ws.ensure(lib().svt_sparse_mla_decode_workspace_size(T, H, K, num_splits))
-        _check(lib().svt_sparse_mla_decode(_ptr(q), T, H, ctypes.byref(kvc), _ptr(bt), 0 if bt is None else bt.shape[0],
+        _check(lib().svt_sparse_mla_decode(_ptr(q), T, H, ctypes.byref(kvc), _table(bt, T), 0 if bt is None else bt.shape[0],
                                            0 if bt is None else bt.shape[1], _ptr(_i32(req_of_token, "req_of_token")),
                                            _ptr(_i32(seq_lens, "seq_lens")), _ptr(topk), K,
                                            _ptr(_i32(topk_len, "topk_len")), float(softmax_scale), _ptr(out), _ptr(lse),

@@ -449,3 +449,23 @@ def test_backward_refused_calls_allocate_nothing(S):
             S.sparse_mla_backward(*args, ws=ws)
         assert e.value.status == status
         assert ws.nbytes == 256 and torch.cuda.max_memory_allocated() == before
+
+
+def test_backward_empty_block_table_is_refused(S):
+    """A table of no requests, or of no pages, resolves nothing (and is not the same as none)."""
+    z = lambda *s, d=torch.bfloat16: torch.zeros(s, dtype=d, device="cuda")  # noqa: E731
+    kv, i32 = S.KVCache(z(64, 576), 64, 1, W.KV_BF16), torch.int32
+    for shape in ((0, 3), (2, 0)):
+        bt = z(*shape, d=i32)
+        for T, refused in ((1, True), (0, False)):
+            q, topk, ws = z(T, 4, 576), z(T, 2, d=i32), S.Workspace()
+            out, lse = z(T, 4, 512), z(T, 4, d=torch.float32)
+            calls = (lambda: S.sparse_mla_decode(q, kv, topk, SCALE, block_table=bt, ws=ws),
+                     lambda: S.resolve_topk_slots(topk, block_table=bt, num_pages=64, ws=ws),
+                     lambda: S.sparse_mla_backward(q, kv, topk, SCALE, out, lse, out, block_table=bt, ws=ws))
+            for call in calls:
+                if refused:
+                    with pytest.raises(S.SvtError, match="num_reqs"):
+                        call()
+                else:
+                    call()
