@@ -267,7 +267,8 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
       const float nm = fmaxf(st.m, block_reduce<true>(make_float4(fill_part(row, a, m, vec, part), 0.f, 0.f, 0.f), sh.red[0]).x);
       const float s = block_reduce<false>(
           make_float4(exp_part<false>(part, m, c, nm == -CUDART_INF_F ? 0.f : nm), 0.f, 0.f, 0.f), sh.red[1]).x;
-      st.s = (st.m == -CUDART_INF_F ? 0.f : st.s * exp2f((st.m - nm) * c)) + s;
+      // (without a largest score so far the sum is 0, or NaN from NaN scores)
+      st.s = (st.m == -CUDART_INF_F ? st.s : st.s * exp2f((st.m - nm) * c)) + s;
       st.m = nm;
     }
     mx = st.m;

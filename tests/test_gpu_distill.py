@@ -245,3 +245,19 @@ def test_distill_weights_of_any_size(S, scope):
     s[:, ::3] = -math.inf
     w[topk % 3 == 0] = 0.0
     check(S, s, lens, topk, w, scope=scope)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_distill_nan_among_masked_scores_of_a_long_row_stays_nan(S, dtype):
+    """Rows so long that a CTA reads its share in pieces; in the first piece nothing but -inf and one NaN."""
+    N, K = 140_000, 16
+    scores, lens, topk, teacher = case(70, 3, N, K, dtype, ragged=False)
+    scores[0, :16384] = -math.inf
+    scores[0, 100] = math.nan
+    scores[2, :16384] = -math.inf  # the same row without the NaN
+    topk[:] += 20_000 * (topk < 20_000).to(torch.int32)
+    loss, grad = S.distill_topk(scores.cuda(), topk.cuda(), teacher.cuda())
+    assert bool(loss[0].isnan()) and bool(grad[0].isnan().all())
+    (rl, rg), (bl, bg) = R.distill(scores[1:], None, topk[1:], teacher[1:], "weights", "candidates", 1.0)
+    R.within(loss[1:], rl, bl, "loss")
+    R.within(grad[1:], rg, bg + R.HALF[dtype] * (rg.abs() + bg) + 2.0 ** -126, "gradient")
