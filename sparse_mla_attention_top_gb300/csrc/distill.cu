@@ -368,8 +368,8 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     add(-log2f(mw));
     const float rest = __fmaf_rn(-quot, W, D) / W;
     const float d = sum + (low + rest);
-    // an infinite sum (a weight on a score of -inf) has no remainder
-    p.loss[t] = some ? (fabsf(quot) == CUDART_INF_F ? quot : d) * 0.6931471805599453f : 0.f;
+    // an infinite sum (a weight on a score of -inf) has no remainder; Z is NaN with NaN scores beside it
+    p.loss[t] = some ? (fabsf(quot) == CUDART_INF_F && Z == Z ? quot : d) * 0.6931471805599453f : 0.f;
   }
   if (drow == nullptr) return;
 

@@ -261,3 +261,16 @@ def test_distill_nan_among_masked_scores_of_a_long_row_stays_nan(S, dtype):
     (rl, rg), (bl, bg) = R.distill(scores[1:], None, topk[1:], teacher[1:], "weights", "candidates", 1.0)
     R.within(loss[1:], rl, bl, "loss")
     R.within(grad[1:], rg, bg + R.HALF[dtype] * (rg.abs() + bg) + 2.0 ** -126, "gradient")
+
+
+@pytest.mark.parametrize("scope,nan_listed", [("candidates", False), ("candidates", True), ("listed", True)])
+@pytest.mark.parametrize("N,K", [(100, 8), (9000, 8), (9000, 2100), (140_000, 8)])
+def test_distill_nan_beside_a_weighted_score_of_minus_infinity(S, scope, nan_listed, N, K):
+    """A NaN makes the row NaN also where a listed score of -inf alone would make its loss infinite."""
+    scores, lens, topk, teacher = case(71, 3, N, K, ragged=False)
+    free = [n for n in range(K + 1) if n not in topk[0].tolist()][0]
+    scores[0, topk[0, 0] if nan_listed else free], scores[0, topk[0, 1]] = math.nan, -math.inf
+    scores[1, topk[1, 1]] = -math.inf
+    loss, grad = S.distill_topk(scores.cuda(), topk.cuda(), teacher.cuda(), over=scope)
+    assert bool(loss[0].isnan()) and float(loss[1]) == math.inf and bool(loss[2].isfinite())
+    assert bool(grad[0, topk[0].long().cuda()].isnan().all()) and bool(grad[1:].isfinite().all())
