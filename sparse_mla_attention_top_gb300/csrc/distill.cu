@@ -10,7 +10,9 @@
 //   e = c ((v - x) - (v_m - m)) (logits) or log2 w - c (x - m) (weights),
 // so one sweep over the list serves the loss. An entry's two logarithms are subtracted before they are
 // summed, which keeps the digits of a small loss of long logarithms, and a list of one entry has
-// exactly no loss and no gradient.
+// exactly no loss and no gradient. Scores may be masks of the type's lowest value: the e's are held times
+// 2^-32, so that one of 3.4e38 and their sum stay finite, and where the whole row is such a mask, x - m is
+// taken first, so that v is not lost in v - x (neither costs time that shows).
 //
 // Bound: reading the scores once and writing the gradient once. A row is cut between the CTAs
 // of a cluster so that each part (up to 64 KB) stays in shared memory: it is read from memory
@@ -36,10 +38,12 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kPart = 16384;  // scores of one part: 64 KB as fp32
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxSplit = 8;
+constexpr float kDown = 1.f / 4294967296.f;  // the e's are held times this
+constexpr float kUp = 4294967296.f;
 
 struct Stats {
   float m, s;  // largest score, sum of 2^(c (x - m)) (this CTA's candidates)
-  float w, d;  // sums of w and of w e (this CTA's share of the list), e as below
+  float w, d;  // sums of w and of w e kDown (this CTA's share of the list), e as below
 };
 
 struct DistillShared {
@@ -292,6 +296,11 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
   }
   float held_w[kHeld];
   {
+    const float ce = c * kDown;
+    // (v - x) - (tmax - ref); beyond 2^10 the differences lose more of v than x - ref loses of x
+    const float base = fabsf(ref) > 1024.f ? ref : 0.f;
+    const float top = tmax - (ref - base);
+    auto gap = [&](float v, float x) { return (v - (x - base)) - top; };
     float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
     if (kAll && kFit) r.x = exp_part<true>(part, n, c, ref);
     entries([&](int u, int, float v, float x) {
@@ -301,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
       // where CTAs see the same entries, each takes every split-th for the sums
       if (!(kAll && kFit) && ((tid + u * kThreads) & (p.split - 1)) != cr) return;
       r.y += w;
-      if (w != 0.f) r.z += w * (p.logits ? ((v - x) - (tmax - ref)) * c : fmaf(ref - x, c, log2f(w)));
+      if (w != 0.f) r.z += w * (p.logits ? gap(v, x) * ce : fmaf(ref - x, ce, log2f(w) * kDown));
     });
     r = block_reduce<false>(r, sh.red[1]);
     if (!(kAll && !kFit)) st.s = r.x;
@@ -338,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
       const float up = kAll && M != -CUDART_INF_F ? (q.m == -CUDART_INF_F ? 0.f : q.m) - M : 0.f;
       if (q.w != 0.f) {
         W += q.w;
-        D += q.d - q.w * (up * c);
+        D += q.d - q.w * (up * (c * kDown));
       }
       if constexpr (kAll) {
         if (q.m != -CUDART_INF_F) Z += q.s * exp2f(up * c);
@@ -357,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     int ez, ew;
     const float mz = frexpf(Z, &ez), mw = frexpf(W, &ew);
     const float quot = __fdiv_rn(D, W);
-    float sum = quot, low = 0.f;
+    float sum = quot * kUp, low = 0.f;
     auto add = [&](float x) {
       const float u = __fadd_rn(sum, x);
       low += fabsf(sum) >= fabsf(x) ? __fadd_rn(__fsub_rn(sum, u), x) : __fadd_rn(__fsub_rn(x, u), sum);
@@ -366,10 +375,11 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     add(static_cast<float>(ez - ew));
     add(log2f(mz));
     add(-log2f(mw));
-    const float rest = __fmaf_rn(-quot, W, D) / W;
-    const float d = sum + (low + rest);
-    // an infinite sum (a weight on a score of -inf) has no remainder; Z is NaN with NaN scores beside it
-    p.loss[t] = some ? (fabsf(quot) == CUDART_INF_F && Z == Z ? quot : d) * 0.6931471805599453f : 0.f;
+    const float rest = __fmaf_rn(-quot, W, D) / W * kUp;
+    const float d = (sum + (low + rest)) * 0.6931471805599453f;
+    // a sum that is infinite in log2 units (a weight on a score of -inf, or on one of the lowest value) leaves
+    // the logarithms nothing to add; Z is NaN with NaN scores beside it
+    p.loss[t] = some ? (fabsf(quot * kUp) == CUDART_INF_F && Z == Z ? quot * 0.6931471805599453f * kUp : d) : 0.f;
   }
   if (drow == nullptr) return;
 

@@ -274,3 +274,32 @@ def test_distill_nan_beside_a_weighted_score_of_minus_infinity(S, scope, nan_lis
     loss, grad = S.distill_topk(scores.cuda(), topk.cuda(), teacher.cuda(), over=scope)
     assert bool(loss[0].isnan()) and float(loss[1]) == math.inf and bool(loss[2].isfinite())
     assert bool(grad[0, topk[0].long().cuda()].isnan().all()) and bool(grad[1:].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("scope", ["candidates", "listed"])
+@pytest.mark.parametrize("kind", ["weights", "logits"])
+@pytest.mark.parametrize("N,K", [(64, 6), (9000, 6), (9000, 2100)])
+def test_distill_listed_scores_of_the_lowest_value(S, dtype, scope, kind, N, K):
+    """Masks of the type's lowest value instead of -inf: a weighted one costs its share of 3.4e38, a finite
+    loss. Its fp32 terms: the difference of scores, c = log2 e / tau (two roundings), the product, the weight
+    (2 ulp and a division), the logarithm below it, W, the quotient and ln 2, each within 2^-23, and sums of
+    at most 2100 / 512 + 64 steps of 2^-24: below 2^-17."""
+    low = torch.finfo(dtype).min
+    scores, lens, topk, teacher = case(72, 4, N, K, dtype, kind, ragged=False)
+    masked = K // 2
+    for t in (0, 1):
+        scores[t, topk[t, :masked].long()] = low
+    scores[2] = low  # every score the same: a uniform softmax
+    if kind == "weights":
+        teacher = teacher * 0.25 + 0.5
+    for tau in (1.0, 8.0):
+        loss, grad = S.distill_topk(scores.cuda(), topk.cuda(), teacher.cuda(), teacher_kind=kind, over=scope, temperature=tau)
+        # (relative to the row's largest: fp64 would lose ln N beside 3.4e38)
+        shifted = scores.double() - scores.double().amax(1, keepdim=True)
+        (rl, rg), _ = R.distill(shifted, None, topk, teacher, kind, scope, tau)
+        assert 1e36 < float(rl[0]) < 3.3e38 and float(rl[2]) < 20
+        off = (loss.double().cpu() - rl).abs()
+        assert bool((off[:2] <= 2.0 ** -17 * rl[:2]).all()), (loss, rl)
+        assert bool((off[2:] <= 1e-4).all()), (loss, rl)
+        assert float((grad.double().cpu() - rg).abs().max()) <= (2.0 ** -17 + R.HALF[dtype]) / tau
