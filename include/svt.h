@@ -334,7 +334,9 @@ SVT_API svt_status svt_rope_frequencies(int32_t dim, double base, const svt_rope
  *                 be x (same strides); otherwise they must not overlap. Rows of out must not overlap.
  *   positions     [T] int32, any value. Angles are reduced modulo a turn in 64-bit fixed point before
  *                 they are rounded to fp32: far positions are as exact as an fp64 product.
- *   freqs         [dim / 2] fp64 device array, radians per position. dim even, at most 512.
+ *   freqs         [dim / 2] fp64 device array, radians per position. dim even, at most 512. An angle is off
+ *                 by at most |pos| (|freq| + 1) 2^-64 turns. NaN, infinities and magnitudes of 2^52 and
+ *                 above are no frequency: their pair's results are NaN.
  *   inverse       non-zero: the angles negated. With the same amplitude this is the transpose, which
  *                 maps the gradient of out to the gradient of x.
  * Arithmetic in fp32, rounded once to dtype. H and D at most 16384, T * H < 2^31. One kernel, no
@@ -358,7 +360,7 @@ SVT_API svt_status svt_rope(const void* x, void* out, svt_dtype dtype, int32_t T
  *                 of zeros) and the codes nearest to value / scale, in IEEE fp32 division. A latent
  *                 value beyond 65504 (or NaN) or a rotated one the f16 arithmetic of that cache cannot
  *                 hold sets SVT_DEV_ERR_FP8_RANGE; the row is written all the same.
- *   freqs         [32] fp64 device array; layout and amplitude as for svt_rope.
+ *   freqs         [32] fp64 device array; freqs, layout and amplitude as for svt_rope.
  *   q_rope, q_out [T, H, 64] bf16 at element strides (t, h): the queries' rope columns, rotated from
  *                 q_rope into q_out (for instance columns 512 .. 575 of q). Both NULL: no queries.
  * Workspace: the 256-byte status header. One kernel. T at most 2^30.

@@ -1,5 +1,8 @@
 """Rotary positions and cache writes on the GPU against an fp64 statement."""
 
+import math
+from fractions import Fraction
+
 import pytest
 import torch
 
@@ -234,3 +237,55 @@ def test_rope_broadcast_input_and_refused_overlapping_output(S):
         S.rope(wide, positions(14, 5).cuda(), f.cuda(), out=wide)
     with pytest.raises(TypeError):
         S.rope(wide, positions(14, 5), f.cuda())  # positions on the CPU
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rope_frequencies_that_are_no_frequency_give_nan(S, layout, dtype):
+    """NaN, infinities and magnitudes of 2^52 and above: NaN in their own pair, the other pairs as ever."""
+    bad = [math.nan, math.inf, -math.inf, 2.0 ** 52, -1e300]
+    f = torch.tensor([0.5, *bad, 0.0, -3.25], dtype=torch.float64)
+    n, T = len(f), 5
+    x, pos = normal(15, T, 2, 2 * n, dtype=dtype), torch.tensor([1, -7, 3, 2 ** 31 - 1, 12], dtype=torch.int32)
+    got = S.rope(x.cuda(), pos.cuda(), f.cuda(), layout=layout).cpu()
+    ok = torch.ones(n, dtype=torch.bool)
+    ok[1: 1 + len(bad)] = False
+    cols = torch.cat([ok, ok]) if layout == "half" else ok.repeat_interleave(2)
+    assert bool(got[..., ~cols].isnan().all())
+    keep = x[..., cols]
+    ref = R.rotate(keep, pos, f[ok], layout)
+    R.within(got[..., cols], ref, R.rotate_bound(keep, ref, layout, dtype, 1.0, pos, f[ok]))
+
+
+def test_rope_append_of_a_frequency_that_is_none_gives_nan(S):
+    f = S.rope_frequencies(64, device="cpu")
+    f[3], f[17] = math.nan, math.inf
+    T = 4
+    lat, kr, pos = normal(16, T, 512), normal(17, T, 64), torch.arange(1, T + 1, dtype=torch.int32)
+    for kind in (W.KV_BF16, W.KV_FP8_E4M3):
+        kv = S.KVCache(torch.zeros(T, S.svt.ROW_BYTES[kind], dtype=torch.uint8, device="cuda"), T, 1, kind)
+        ws = S.Workspace()
+        S.rope_append(lat.cuda(), kr.cuda(), pos.cuda(), (pos - 1).cuda(), kv, f.cuda(), layout="half", ws=ws)
+        values = cache_values(kv.data.cpu(), kind)
+        rope = values[:, 512:] if kind == W.KV_BF16 else values[2]
+        bad = torch.zeros(64, dtype=torch.bool)
+        bad[[3, 17, 35, 49]] = True
+        assert torch.equal(rope.isnan(), bad.expand(T, 64))
+
+
+def test_rope_large_frequencies_to_the_documented_error(S):
+    """|pos| (|freq| + 1) 2^-64 turns, next to the fp32 roundings: against the angle modulo a turn from exact
+    fractions and 50 digits of pi."""
+    pi = Fraction(31415926535897932384626433832795028841971693993751, 10 ** 49)
+    f = torch.tensor([2.0 ** 20 + 1 / 3, -(2.0 ** 33) - 0.7, 2.0 ** 45 + 9, 2.0 ** 52 - 1], dtype=torch.float64)
+    pos = torch.tensor([1, -3, 1000, 2 ** 31 - 1], dtype=torch.int32)
+    x = normal(18, len(pos), 1, 2 * len(f), dtype=torch.float32)
+    got = S.rope(x.cuda(), pos.cuda(), f.cuda()).cpu().double()
+    for t in range(len(pos)):
+        for i in range(len(f)):
+            turns = Fraction(int(pos[t])) * Fraction(float(f[i])) / (2 * pi)
+            a = float((turns - round(turns)) * 2 * pi)
+            u, v = x[t, 0, 2 * i].double(), x[t, 0, 2 * i + 1].double()
+            off = 2 * math.pi * abs(int(pos[t])) * (abs(float(f[i])) + 1) * 2.0 ** -64 + 2.0 ** -21
+            assert abs(got[t, 0, 2 * i] - (u * math.cos(a) - v * math.sin(a))) <= off * (abs(u) + abs(v))
+            assert abs(got[t, 0, 2 * i + 1] - (u * math.sin(a) + v * math.cos(a))) <= off * (abs(u) + abs(v))
