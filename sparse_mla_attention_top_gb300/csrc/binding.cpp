@@ -299,17 +299,18 @@ PyObject* distill(PyObject* const* a) {
   return t;
 }
 
-// capture_id(stream address): the id of the capture that records the stream (0 = none)
-PyObject* capture_id(PyObject* const* a) {
-  const auto stream = reinterpret_cast<cudaStream_t>(static_cast<uintptr_t>(integer(a[0])));
+// where(): (current device, address of its current stream, id of the capture that records the stream or 0)
+PyObject* where(PyObject* const*) {
+  const int device = c10::cuda::current_device();
+  const auto stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
   cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
   unsigned long long id = 0;
   if (cudaStreamGetCaptureInfo(stream, &status, &id) != cudaSuccess) {
-    (void)cudaGetLastError();
-    PyErr_SetString(PyExc_RuntimeError, "the stream's capture cannot be queried");
-    throw PyFailure{};
+    (void)cudaGetLastError();  // the legacy stream beside a capture: no call can be enqueued there, which it will say
+    status = cudaStreamCaptureStatusNone;
   }
-  return PyLong_FromUnsignedLongLong(status == cudaStreamCaptureStatusNone ? 0 : id);
+  return Py_BuildValue("(iKK)", device, static_cast<unsigned long long>(reinterpret_cast<uintptr_t>(stream)),
+                       status == cudaStreamCaptureStatusNone ? 0ull : id);
 }
 
 // Calls `f` with its arguments; no C++ exception leaves.
@@ -348,7 +349,7 @@ PyObject* bind(PyObject* const* a) {
 #define SVT_METHOD(name, f, n, bound) \
   {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<f, n, bound>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {SVT_METHOD("bind", bind, 5, false),
-                         SVT_METHOD("capture_id", capture_id, 1, false),
+                         SVT_METHOD("where", where, 0, false),
                          SVT_METHOD("rope", rope, 8, true),
                          SVT_METHOD("rope_append", rope_append, 15, true),
                          SVT_METHOD("sparse_mla_backward", backward, 20, true),

@@ -185,21 +185,25 @@ class Workspace:
         self.lock = threading.RLock()
 
     def ensure(self, nbytes: int) -> "Workspace":
-        """At least nbytes. Every call makes this one, under the lock, before it takes ptr and nbytes."""
+        """At least nbytes."""
         with self.lock:
-            capturing = self.buf.is_cuda and torch.cuda.is_current_stream_capturing()
-            if nbytes > self.buf.numel():
-                old = self.buf
-                self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
-                if self._captured or capturing:
-                    self._kept.append(old)
-                else:
-                    self.buf[:256].copy_(old[:256])  # keep pending status bits
-                    if old.is_cuda:
-                        old.record_stream(torch.cuda.current_stream())  # earlier calls may still run
-                self._captured = False
-            self._captured |= capturing
+            self._size_to(nbytes, self.buf.is_cuda and torch.cuda.is_current_stream_capturing())
         return self
+
+    def _size_to(self, nbytes: int, capturing: bool) -> None:
+        """What a call makes of its workspace, under the lock, before it takes ptr and nbytes."""
+        if nbytes > self.buf.numel():
+            old = self.buf
+            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            if self._captured or capturing:
+                self._kept.append(old)
+            else:
+                self.buf[:256].copy_(old[:256])  # keep pending status bits
+                if old.is_cuda:
+                    old.record_stream(torch.cuda.current_stream())  # earlier calls may still run
+            self._captured = False
+        if capturing:
+            self._captured = True
 
     @property
     def ptr(self):
@@ -218,9 +222,24 @@ class Workspace:
         return bits
 
 
-_default_ws = {}   # (device, stream) -> Workspace
-_captured_ws = {}  # (device, stream) -> (id of its last capture, Workspace)
+_default_ws = {}  # (device, stream, capture or 0) -> Workspace
 _default_lock = threading.Lock()
+
+
+def _workspace(ws: Optional[Workspace]):
+    """The workspace of a call (the given one, or the default), and whether the call is captured."""
+    at = (_fast or _binding()).where()
+    if ws is None:
+        ws = _default_ws.get(at)
+        if ws is None:
+            with _default_lock:
+                ws = _default_ws.get(at)
+                if ws is None:
+                    if at[2]:  # a stream's last capture is over, and its graph's memory the graph's own
+                        for key in [k for k in _default_ws if k[:2] == at[:2] and k[2]]:
+                            del _default_ws[key]
+                    ws = _default_ws[at] = Workspace()
+    return ws, at[2] != 0
 
 
 def default_workspace() -> Workspace:
@@ -228,23 +247,7 @@ def default_workspace() -> Workspace:
     streams may overlap. While the stream is being captured it is one of that capture's own, as two graphs
     may be replayed at once: it lies in the graph's memory, and each replay begins by clearing its status.
     Give captured calls a workspace where their status is to be read."""
-    dev = torch.cuda.current_device()
-    stream = torch._C._cuda_getCurrentRawStream(dev)
-    if torch.cuda.is_current_stream_capturing():
-        capture = _binding().capture_id(stream)
-        with _default_lock:
-            last, ws = _captured_ws.get((dev, stream), (None, None))
-            if last != capture:
-                ws = Workspace()
-                _captured_ws[dev, stream] = capture, ws
-        return ws
-    ws = _default_ws.get((dev, stream))
-    if ws is None:
-        with _default_lock:
-            ws = _default_ws.get((dev, stream))
-            if ws is None:
-                ws = _default_ws[dev, stream] = Workspace()
-    return ws
+    return _workspace(None)[0]
 
 
 def resolve_topk_slots(topk_pos, *, block_table=None, seq_lens=None, req_of_token=None, topk_len=None,
@@ -254,9 +257,9 @@ def resolve_topk_slots(topk_pos, *, block_table=None, seq_lens=None, req_of_toke
     T, K = topk_pos.shape
     bt = _i32(block_table, "block_table")
     out = torch.empty((T, K), dtype=torch.int32, device=topk_pos.device) if out is None else out
-    ws = ws or default_workspace()
+    ws, capturing = _workspace(ws)
     with ws.lock:
-        ws.ensure(lib().svt_resolve_workspace_size())
+        ws._size_to(lib().svt_resolve_workspace_size(), capturing)
         _check(lib().svt_resolve_topk_slots(_ptr(topk_pos), T, K, _ptr(_i32(topk_len, "topk_len")),
                                             _ptr(_i32(req_of_token, "req_of_token")), _table(bt, T),
                                             0 if bt is None else bt.shape[0], 0 if bt is None else bt.shape[1],
@@ -280,10 +283,10 @@ def sparse_mla_decode(q, kv: KVCache, topk, softmax_scale: float, *, block_table
         out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=q.device)
     if lse is None and return_lse:
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    ws = ws or default_workspace()
+    ws, capturing = _workspace(ws)
     kvc = kv._c()
     with ws.lock:
-        ws.ensure(lib().svt_sparse_mla_decode_workspace_size(T, H, K, num_splits))
+        ws._size_to(lib().svt_sparse_mla_decode_workspace_size(T, H, K, num_splits), capturing)
         _check(lib().svt_sparse_mla_decode(_ptr(q), T, H, ctypes.byref(kvc), _table(bt, T), 0 if bt is None else bt.shape[0],
                                            0 if bt is None else bt.shape[1], _ptr(_i32(req_of_token, "req_of_token")),
                                            _ptr(_i32(seq_lens, "seq_lens")), _ptr(topk), K,
@@ -302,9 +305,9 @@ def build_group_union(slots, G: int, num_slots: int, *, topk_len=None, enc=None,
         enc = torch.empty((groups, G * K), dtype=torch.int32, device=slots.device)
     if lens is None:
         lens = torch.empty((groups,), dtype=torch.int32, device=slots.device)
-    ws = ws or default_workspace()
+    ws, capturing = _workspace(ws)
     with ws.lock:
-        ws.ensure(lib().svt_build_group_union_workspace_size(T, K, G))
+        ws._size_to(lib().svt_build_group_union_workspace_size(T, K, G), capturing)
         _check(lib().svt_build_group_union(_ptr(slots), _ptr(_i32(topk_len, "topk_len")), T, K, int(G), int(num_slots),
                                            _ptr(enc), _ptr(lens), ws.ptr, ws.nbytes, _stream()), "svt_build_group_union")
     return enc, lens
@@ -322,11 +325,11 @@ def sparse_mla_prefill_grouped(q, G: int, kv: KVCache, enc, lens, K: int, softma
         out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=q.device)
     if lse is None and return_lse:
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    ws = ws or default_workspace()
+    ws, capturing = _workspace(ws)
     kvc = kv._c()
     name = "svt_sparse_mla_prefill_grouped_union_tile" if union_tile else "svt_sparse_mla_prefill_grouped"
     with ws.lock:
-        ws.ensure(lib().svt_sparse_mla_prefill_grouped_workspace_size(T, H, G))
+        ws._size_to(lib().svt_sparse_mla_prefill_grouped_workspace_size(T, H, G), capturing)
         _check(getattr(lib(), name)(_ptr(q), T, H, int(G), ctypes.byref(kvc), _ptr(_i32(enc, "enc")),
                                     _ptr(_i32(lens, "lens")), int(K), float(softmax_scale), _ptr(out), _ptr(lse), ws.ptr,
                                     ws.nbytes, _stream()), name)
@@ -422,9 +425,9 @@ def rope_append(latent, k_rope, positions, slots, kv: KVCache, freqs, *, layout:
     strided) to cache rows slots [T] (negative: skipped); with q_rope [T, H, 64] it rotates the
     queries' rope columns into q_out (a new tensor when None; q[..., 512:] of a [T, H, 576] q fits)
     in the same launch. Returns q_out."""
-    ws = ws or default_workspace()
+    ws, capturing = _workspace(ws)
     with ws.lock:
-        ws.ensure(256)
+        ws._size_to(256, capturing)
         r = (_fast or _binding()).rope_append(latent, k_rope, positions, slots, kv.data, kv.num_pages, kv.page_size,
                                               kv.row_stride_bytes, kv.dtype, freqs, _choice(layout, ROPE_LAYOUTS, "layout"),
                                               amplitude, q_rope, q_out, ws.buf)
@@ -439,9 +442,9 @@ def sparse_mla_backward(q, kv: KVCache, topk, softmax_scale: float, out, lse, do
     """svt_sparse_mla_backward: the gradients of sparse_mla_decode (or of a grouped prefill, with each
     query's own list). out and lse are the forward's; dout (and dlse) their gradients. Returns
     (dq [T, H, 576] bf16, dkv [num_slots, 576] bf16, weights [T, K] fp32 or None)."""
-    ws = ws or default_workspace()
+    ws, capturing = _workspace(ws)
     with ws.lock:
-        ws.ensure(256)
+        ws._size_to(256, capturing)
         for _ in range(2):
             r = (_fast or _binding()).sparse_mla_backward(
                 q, kv.data, kv.num_pages, kv.page_size, kv.row_stride_bytes, kv.dtype, topk, softmax_scale, out, lse, dout,
@@ -450,7 +453,7 @@ def sparse_mla_backward(q, kv: KVCache, topk, softmax_scale: float, out, lse, do
                 return r
             if r >= 0:
                 break
-            ws.ensure(-r)
+            ws._size_to(-r, capturing)
     _check(r, "svt_sparse_mla_backward")
 
 
@@ -481,10 +484,10 @@ def gather_probe(kv: KVCache, slots, mode: int = 0, *, out=None, ws: Optional[Wo
     n = slots.numel()
     if out is None:
         out = torch.empty((n,), dtype=torch.int32, device=slots.device)
-    ws = default_workspace() if ws is None else ws
+    ws, capturing = _workspace(ws)
     kvc = kv._c()
     with ws.lock:
-        ws.ensure(256)
+        ws._size_to(256, capturing)
         _check(lib().svt_gather_probe(ctypes.byref(kvc), _ptr(slots), n, int(mode), _ptr(out), ws.ptr, ws.nbytes,
                                       _stream()), "svt_gather_probe")
     return out
@@ -501,9 +504,9 @@ def tensor_probe(k_rows, q, pt, reps: int = 1, grid: int = 1, *, ws: Optional[Wo
     s_out = torch.empty((64, 64), dtype=torch.float32, device=dev)
     o_out = torch.empty((512, 64), dtype=torch.float32, device=dev)
     cycles = torch.empty((int(grid),), dtype=torch.int64, device=dev)
-    ws = default_workspace() if ws is None else ws
+    ws, capturing = _workspace(ws)
     with ws.lock:
-        ws.ensure(256)
+        ws._size_to(256, capturing)
         _check(lib().svt_tensor_probe(_ptr(k_rows), _ptr(q), _ptr(pt), int(reps), int(grid), _ptr(s_out), _ptr(o_out),
                                       _ptr(cycles), ws.ptr, ws.nbytes, _stream()), "svt_tensor_probe")
     return s_out, o_out, cycles

@@ -199,19 +199,14 @@ def test_the_binding_refuses_what_is_no_tensor(L):
 
 def test_default_workspaces_are_one_a_stream_and_one_a_capture(monkeypatch):
     """A workspace is scratch for one stream: calls on two streams, or in two graphs, may overlap."""
-    at = dict(device=0, stream=0, capture=0)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: at["device"])
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: at["stream"], raising=False)
-    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: at["capture"] != 0)
-    monkeypatch.setattr(svt, "_binding", lambda: type("B", (), {"capture_id": staticmethod(lambda s: at["capture"])}))
+    at = [0, 0, 0]
+    monkeypatch.setattr(svt, "_fast", type("B", (), {"where": staticmethod(lambda: tuple(at))}))
     made = svt.Workspace
     monkeypatch.setattr(svt, "Workspace", lambda: made("cpu"))
     monkeypatch.setattr(svt, "_default_ws", {})
-    monkeypatch.setattr(svt, "_captured_ws", {}, raising=False)
 
-    def ws(**kw):
-        at.update(device=0, stream=0, capture=0)
-        at.update(kw)
+    def ws(device=0, stream=0, capture=0):
+        at[:] = device, stream, capture
         return svt.default_workspace()
     plain = ws()
     assert ws() is plain and ws(stream=7) is ws(stream=7)
