@@ -187,9 +187,15 @@ bool encode_q_map(AttnParams& p, long long rows) {
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kRow) * 2};
   const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(kRowsetRows)};
   const cuuint32_t elem_strides[2] = {1, 1};
-  return g_encode_tiled(&p.q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(p.q), dims, strides, box,
-                        elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  auto encode = [&] {
+    return g_encode_tiled(&p.q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(p.q), dims, strides,
+                          box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (encode()) return true;
+  // a driver call needs a context; a thread that has made no runtime call yet gets its device's here
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
 }
 
 void debug_fault_state(int* fault, unsigned long long* wait_limit_ns) {

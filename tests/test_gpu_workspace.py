@@ -138,3 +138,31 @@ def test_outgrown_buffers_are_kept_for_captured_calls_alone(S):
     g.replay()
     assert ws.read_status() == S.svt.DEV_ERR_INDEX_RANGE and ws.read_status() == 0
     del junk
+
+
+@pytest.mark.parametrize("name", ["decode", "split", "unsplit", "prefill", "backward"])
+def test_the_first_call_of_a_thread(S, name):
+    """A new thread that has made no CUDA call of its own."""
+    step = Step(S, 9, T=8, H=16)
+    ws = S.Workspace(nbytes=1 << 24)
+    out = torch.empty_like(step.want[0]), torch.empty_like(step.want[1])
+    enc, lens = S.build_group_union(step.topk, 8, step.kv.num_slots, ws=ws)
+    decode = lambda n: S.sparse_mla_decode(step.q, step.kv, step.topk, SCALE, num_splits=n, out=out[0], lse=out[1], ws=ws)  # noqa: E731
+    call = {"decode": lambda: decode(0), "split": lambda: decode(3), "unsplit": lambda: decode(1),
+            "prefill": lambda: S.sparse_mla_prefill_grouped(step.q, 8, step.kv, enc, lens, 300, SCALE, out=out[0], lse=out[1],
+                                                            ws=ws),
+            "backward": lambda: S.sparse_mla_backward(step.q, step.kv, step.topk, SCALE, *step.want[:2], step.dout, ws=ws)}[name]
+    errors = []
+
+    def run():
+        try:
+            call()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+    t = threading.Thread(target=run)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    if name != "backward":
+        assert float((out[1] - step.want[1]).abs().max()) <= 1e-3
