@@ -1,6 +1,7 @@
 // C ABI of the operators around the attention: rotary positions, cache writes, the attention's
 // backward pass and the indexer's distillation loss. As everywhere in the library, every check
 // comes before anything is enqueued, and nothing allocates device memory or waits for a stream.
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -58,10 +59,15 @@ bool rows_overlap(int32_t T, int32_t H, int32_t D, int64_t st, int64_t sh) {
   return false;
 }
 
+// Of the current device; asked for two or three times by a backward call, so known ones are kept.
 int sm_count() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < kDevices && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < kDevices) known[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
 

@@ -305,8 +305,9 @@ PyObject* where(PyObject* const*) {
   const auto stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
   cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
   unsigned long long id = 0;
-  if (cudaStreamGetCaptureInfo(stream, &status, &id) != cudaSuccess) {
-    (void)cudaGetLastError();  // the legacy stream beside a capture: no call can be enqueued there, which it will say
+  // (the legacy stream cannot be captured)
+  if (stream != nullptr && cudaStreamGetCaptureInfo(stream, &status, &id) != cudaSuccess) {
+    (void)cudaGetLastError();
     status = cudaStreamCaptureStatusNone;
   }
   return Py_BuildValue("(iKK)", device, static_cast<unsigned long long>(reinterpret_cast<uintptr_t>(stream)),

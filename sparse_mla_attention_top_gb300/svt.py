@@ -227,7 +227,8 @@ _default_lock = threading.Lock()
 
 
 def _workspace(ws: Optional[Workspace]):
-    """The workspace of a call (the given one, or the default), and whether the call is captured."""
+    """The workspace of a call (the given one, or the default), whether the call is captured, and the
+    address of its stream."""
     at = (_fast or _binding()).where()
     if ws is None:
         ws = _default_ws.get(at)
@@ -239,7 +240,7 @@ def _workspace(ws: Optional[Workspace]):
                         for key in [k for k in _default_ws if k[:2] == at[:2] and k[2]]:
                             del _default_ws[key]
                     ws = _default_ws[at] = Workspace()
-    return ws, at[2] != 0
+    return ws, at[2] != 0, at[1]
 
 
 def default_workspace() -> Workspace:
@@ -257,14 +258,14 @@ def resolve_topk_slots(topk_pos, *, block_table=None, seq_lens=None, req_of_toke
     T, K = topk_pos.shape
     bt = _i32(block_table, "block_table")
     out = torch.empty((T, K), dtype=torch.int32, device=topk_pos.device) if out is None else out
-    ws, capturing = _workspace(ws)
+    ws, capturing, stream = _workspace(ws)
     with ws.lock:
         ws._size_to(lib().svt_resolve_workspace_size(), capturing)
         _check(lib().svt_resolve_topk_slots(_ptr(topk_pos), T, K, _ptr(_i32(topk_len, "topk_len")),
                                             _ptr(_i32(req_of_token, "req_of_token")), _table(bt, T),
                                             0 if bt is None else bt.shape[0], 0 if bt is None else bt.shape[1],
                                             _ptr(_i32(seq_lens, "seq_lens")), int(page_size), int(num_pages), _ptr(out),
-                                            ws.ptr, ws.nbytes, _stream()), "svt_resolve_topk_slots")
+                                            ws.ptr, ws.nbytes, stream), "svt_resolve_topk_slots")
     return out
 
 
@@ -283,7 +284,7 @@ def sparse_mla_decode(q, kv: KVCache, topk, softmax_scale: float, *, block_table
         out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=q.device)
     if lse is None and return_lse:
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    ws, capturing = _workspace(ws)
+    ws, capturing, stream = _workspace(ws)
     kvc = kv._c()
     with ws.lock:
         ws._size_to(lib().svt_sparse_mla_decode_workspace_size(T, H, K, num_splits), capturing)
@@ -291,7 +292,7 @@ def sparse_mla_decode(q, kv: KVCache, topk, softmax_scale: float, *, block_table
                                            0 if bt is None else bt.shape[1], _ptr(_i32(req_of_token, "req_of_token")),
                                            _ptr(_i32(seq_lens, "seq_lens")), _ptr(topk), K,
                                            _ptr(_i32(topk_len, "topk_len")), float(softmax_scale), _ptr(out), _ptr(lse),
-                                           int(num_splits), ws.ptr, ws.nbytes, _stream()), "svt_sparse_mla_decode")
+                                           int(num_splits), ws.ptr, ws.nbytes, stream), "svt_sparse_mla_decode")
     return out, lse
 
 
@@ -305,11 +306,11 @@ def build_group_union(slots, G: int, num_slots: int, *, topk_len=None, enc=None,
         enc = torch.empty((groups, G * K), dtype=torch.int32, device=slots.device)
     if lens is None:
         lens = torch.empty((groups,), dtype=torch.int32, device=slots.device)
-    ws, capturing = _workspace(ws)
+    ws, capturing, stream = _workspace(ws)
     with ws.lock:
         ws._size_to(lib().svt_build_group_union_workspace_size(T, K, G), capturing)
         _check(lib().svt_build_group_union(_ptr(slots), _ptr(_i32(topk_len, "topk_len")), T, K, int(G), int(num_slots),
-                                           _ptr(enc), _ptr(lens), ws.ptr, ws.nbytes, _stream()), "svt_build_group_union")
+                                           _ptr(enc), _ptr(lens), ws.ptr, ws.nbytes, stream), "svt_build_group_union")
     return enc, lens
 
 
@@ -325,14 +326,14 @@ def sparse_mla_prefill_grouped(q, G: int, kv: KVCache, enc, lens, K: int, softma
         out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=q.device)
     if lse is None and return_lse:
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    ws, capturing = _workspace(ws)
+    ws, capturing, stream = _workspace(ws)
     kvc = kv._c()
     name = "svt_sparse_mla_prefill_grouped_union_tile" if union_tile else "svt_sparse_mla_prefill_grouped"
     with ws.lock:
         ws._size_to(lib().svt_sparse_mla_prefill_grouped_workspace_size(T, H, G), capturing)
         _check(getattr(lib(), name)(_ptr(q), T, H, int(G), ctypes.byref(kvc), _ptr(_i32(enc, "enc")),
                                     _ptr(_i32(lens, "lens")), int(K), float(softmax_scale), _ptr(out), _ptr(lse), ws.ptr,
-                                    ws.nbytes, _stream()), name)
+                                    ws.nbytes, stream), name)
     return out, lse
 
 
@@ -425,7 +426,7 @@ def rope_append(latent, k_rope, positions, slots, kv: KVCache, freqs, *, layout:
     strided) to cache rows slots [T] (negative: skipped); with q_rope [T, H, 64] it rotates the
     queries' rope columns into q_out (a new tensor when None; q[..., 512:] of a [T, H, 576] q fits)
     in the same launch. Returns q_out."""
-    ws, capturing = _workspace(ws)
+    ws, capturing, _ = _workspace(ws)
     with ws.lock:
         ws._size_to(256, capturing)
         r = (_fast or _binding()).rope_append(latent, k_rope, positions, slots, kv.data, kv.num_pages, kv.page_size,
@@ -442,7 +443,7 @@ def sparse_mla_backward(q, kv: KVCache, topk, softmax_scale: float, out, lse, do
     """svt_sparse_mla_backward: the gradients of sparse_mla_decode (or of a grouped prefill, with each
     query's own list). out and lse are the forward's; dout (and dlse) their gradients. Returns
     (dq [T, H, 576] bf16, dkv [num_slots, 576] bf16, weights [T, K] fp32 or None)."""
-    ws, capturing = _workspace(ws)
+    ws, capturing, _ = _workspace(ws)
     with ws.lock:
         ws._size_to(256, capturing)
         for _ in range(2):
@@ -484,12 +485,12 @@ def gather_probe(kv: KVCache, slots, mode: int = 0, *, out=None, ws: Optional[Wo
     n = slots.numel()
     if out is None:
         out = torch.empty((n,), dtype=torch.int32, device=slots.device)
-    ws, capturing = _workspace(ws)
+    ws, capturing, stream = _workspace(ws)
     kvc = kv._c()
     with ws.lock:
         ws._size_to(256, capturing)
         _check(lib().svt_gather_probe(ctypes.byref(kvc), _ptr(slots), n, int(mode), _ptr(out), ws.ptr, ws.nbytes,
-                                      _stream()), "svt_gather_probe")
+                                      stream), "svt_gather_probe")
     return out
 
 
@@ -504,9 +505,9 @@ def tensor_probe(k_rows, q, pt, reps: int = 1, grid: int = 1, *, ws: Optional[Wo
     s_out = torch.empty((64, 64), dtype=torch.float32, device=dev)
     o_out = torch.empty((512, 64), dtype=torch.float32, device=dev)
     cycles = torch.empty((int(grid),), dtype=torch.int64, device=dev)
-    ws, capturing = _workspace(ws)
+    ws, capturing, stream = _workspace(ws)
     with ws.lock:
         ws._size_to(256, capturing)
         _check(lib().svt_tensor_probe(_ptr(k_rows), _ptr(q), _ptr(pt), int(reps), int(grid), _ptr(s_out), _ptr(o_out),
-                                      _ptr(cycles), ws.ptr, ws.nbytes, _stream()), "svt_tensor_probe")
+                                      _ptr(cycles), ws.ptr, ws.nbytes, stream), "svt_tensor_probe")
     return s_out, o_out, cycles
