@@ -57,6 +57,12 @@ float real(PyObject* o) {
   return static_cast<float>(v);
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw PyFailure{};
+  return v != 0;
+}
+
 // The address of a contiguous tensor of this type and shape; null for null.
 void* shaped(const at::Tensor* t, const char* name, at::ScalarType type, std::initializer_list<int64_t> shape) {
   if (t == nullptr) return nullptr;
@@ -139,7 +145,7 @@ PyObject* rope(PyObject* const* a) {
       g_rope(x.data_ptr(), out.data_ptr(), type == at::kFloat ? SVT_F32 : SVT_BF16, int32(r.T), int32(r.H), int32(r.D),
              r.st, r.sh, o.st, o.sh, static_cast<const int32_t*>(at), static_cast<const double*>(fr),
              int32(2 * freqs.numel()), int32(integer(a[3])), static_cast<svt_rope_layout>(integer(a[4])), real(a[6]),
-             PyObject_IsTrue(a[5]), stream);
+             truth(a[5]), stream);
   if (st != SVT_OK) return PyLong_FromLong(st);
   return given ? same(a[7]) : wrap(made);
 }
@@ -249,7 +255,7 @@ PyObject* backward(PyObject* const* a) {
     made_kv = at::empty({n, 576}, q.options());
     p_dkv = made_kv.data_ptr();
   }
-  if (PyObject_IsTrue(a[18])) weights = at::empty({T, K}, lse.options());
+  if (truth(a[18])) weights = at::empty({T, K}, lse.options());
   st = call(p_dq, p_dkv, weights.defined() ? static_cast<float*>(weights.data_ptr()) : nullptr, ws.nbytes());
   if (st != SVT_OK) return PyLong_FromLong(st);
   PyObject* r = PyTuple_New(3);
@@ -281,7 +287,7 @@ PyObject* distill(PyObject* const* a) {
   const void* p_rw = shaped(rw, "row_weight", at::kFloat, {T});
   at::Tensor loss = at::empty({T}, x.options().dtype(at::kFloat)), made;
   const at::Tensor* grad = given;
-  if (grad == nullptr && PyObject_IsTrue(a[8])) {
+  if (grad == nullptr && truth(a[8])) {
     made = at::empty({T, N}, x.options());
     grad = &made;
   }

@@ -289,3 +289,12 @@ def test_rope_large_frequencies_to_the_documented_error(S):
             off = 2 * math.pi * abs(int(pos[t])) * (abs(float(f[i])) + 1) * 2.0 ** -64 + 2.0 ** -21
             assert abs(got[t, 0, 2 * i] - (u * math.cos(a) - v * math.sin(a))) <= off * (abs(u) + abs(v))
             assert abs(got[t, 0, 2 * i + 1] - (u * math.sin(a) + v * math.cos(a))) <= off * (abs(u) + abs(v))
+
+
+def test_rope_an_option_without_a_truth_value_is_refused_as_python_does(S):
+    x, pos = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        S.rope(x, pos, S.rope_frequencies(64), inverse=torch.tensor([1, 0]))
+    z = torch.zeros(1, 4, device="cuda")
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        S.distill_topk(z, pos[None], z[:, :1], need_grad=torch.tensor([1, 0]))
