@@ -9,6 +9,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <cuda_runtime_api.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
@@ -335,8 +336,8 @@ PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return f(args);
   } catch (const PyFailure&) {
     return nullptr;
-  } catch (const std::exception& e) {
-    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (const std::exception&) {
+    if (!PyErr_Occurred()) torch::translate_exception_to_python(std::current_exception());  // out of memory as torch's own
     return nullptr;
   }
 }

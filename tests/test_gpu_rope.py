@@ -298,3 +298,10 @@ def test_rope_an_option_without_a_truth_value_is_refused_as_python_does(S):
     z = torch.zeros(1, 4, device="cuda")
     with pytest.raises(RuntimeError, match="ambiguous"):
         S.distill_topk(z, pos[None], z[:, :1], need_grad=torch.tensor([1, 0]))
+
+
+def test_rope_out_of_memory_is_torch_s_error(S):
+    """An output of 2^46 bytes (nothing is allocated, nor launched)."""
+    x = torch.zeros(1, 1, 16384, dtype=torch.bfloat16, device="cuda").expand(131071, 16384, 16384)
+    with pytest.raises(torch.cuda.OutOfMemoryError):
+        S.rope(x, torch.zeros(131071, dtype=torch.int32, device="cuda"), S.rope_frequencies(64))
