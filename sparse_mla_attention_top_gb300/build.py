@@ -35,6 +35,13 @@ def _nvcc() -> str:
     return "nvcc"
 
 
+def binding_target() -> str:
+    """What a binding is good for: the Python and the torch whose headers it was compiled against."""
+    import torch
+
+    return f"Python {sys.version_info.major}.{sys.version_info.minor}, torch {torch.__version__}"
+
+
 def _binding_command(out: Path) -> list:
     import torch
 
@@ -44,12 +51,14 @@ def _binding_command(out: Path) -> list:
                cuda / "include", INCLUDE]
     libs = ["torch_python", "torch", "torch_cpu", "torch_cuda", "c10", "c10_cuda"]
     return ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", str(BINDING_SOURCE), "-o", str(out),
+            f'-DSVT_BINDING_TARGET="{binding_target()}"',
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-isystem{i}" for i in include),
             f"-L{root / 'lib'}", f"-Wl,-rpath,{root / 'lib'}", *(f"-l{name}" for name in libs)]
 
 
 def binding_up_to_date() -> bool:
-    if not BINDING.exists():
+    # (its text holds the target's name, so that no other Python or torch has to load it to find out)
+    if not BINDING.exists() or binding_target().encode() + b"\0" not in BINDING.read_bytes():
         return False
     t = BINDING.stat().st_mtime
     return all(p.stat().st_mtime <= t for p in (BINDING_SOURCE, INCLUDE / "svt.h", Path(__file__)))

@@ -367,4 +367,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&module);
+  // what it was compiled for: the caller compares it with what runs
+  if (m != nullptr && PyModule_AddStringConstant(m, "target", SVT_BINDING_TARGET) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

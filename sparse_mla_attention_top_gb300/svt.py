@@ -378,11 +378,16 @@ def _binding():
     global _fast
     if _fast is None:
         L = lib()
+        from . import build
         try:
             from . import _binding as fast
         except ImportError as e:
             raise RuntimeError("_binding.so is missing or stale: build it first "
                                "(sparse_mla_attention_top_gb300.build)") from e
+        here = build.binding_target()
+        if getattr(fast, "target", None) != here:
+            raise RuntimeError(f"_binding.so was built for {getattr(fast, 'target', 'another torch')}, this is {here}: "
+                               "build it again (sparse_mla_attention_top_gb300.build)")
         fast.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             L.svt_rope, L.svt_rope_append, L.svt_sparse_mla_backward_workspace_size, L.svt_sparse_mla_backward,
             L.svt_distill_topk)))

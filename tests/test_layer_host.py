@@ -263,3 +263,14 @@ def test_page_counts_whose_rows_wrap_round_are_refused(L):
                                          None, None, None, None, None, WS, 1 << 50, None) == (svt.SVT_ERR_INVALID_ARG if ok else uns)
         assert L.svt_resolve_topk_slots(None, 0, 0, None, None, None, 0, 0, None, size, pages, None, WS, 256, None) in (
             (svt.SVT_OK, svt.SVT_ERR_CUDA) if ok else (uns,))
+
+
+def test_a_binding_for_another_torch_is_stale(L, monkeypatch):
+    """Its file times say nothing of what it was compiled against."""
+    assert B.binding_up_to_date() and svt._binding().target == B.binding_target()
+    for name in ("2.1", B.binding_target() + "1", B.binding_target()[:-1]):
+        monkeypatch.setattr(B, "binding_target", lambda: name)
+        assert not B.binding_up_to_date()
+        monkeypatch.setattr(svt, "_fast", None)
+        with pytest.raises(RuntimeError, match="built for"):
+            svt._binding()
