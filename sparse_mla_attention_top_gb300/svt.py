@@ -179,10 +179,15 @@ class Workspace:
 
     def __init__(self, device=None, nbytes: int = 256):
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-        self.buf = torch.zeros(max(256, nbytes), dtype=torch.uint8, device=self.device)
+        self.buf = self._new(max(256, nbytes))
+        self.buf[:256].zero_()
         self._captured = False  # whether a captured call uses buf
         self._kept = []
         self.lock = threading.RLock()
+
+    def _new(self, nbytes: int) -> torch.Tensor:
+        """Only the status header needs a value."""
+        return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
 
     def ensure(self, nbytes: int) -> "Workspace":
         """At least nbytes."""
@@ -194,8 +199,9 @@ class Workspace:
         """What a call makes of its workspace, under the lock, before it takes ptr and nbytes."""
         if nbytes > self.buf.numel():
             old = self.buf
-            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            self.buf = self._new(nbytes)
             if self._captured or capturing:
+                self.buf[:256].zero_()
                 self._kept.append(old)
             else:
                 self.buf[:256].copy_(old[:256])  # keep pending status bits

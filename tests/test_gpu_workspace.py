@@ -166,3 +166,40 @@ def test_the_first_call_of_a_thread(S, name):
     assert not errors
     if name != "backward":
         assert float((out[1] - step.want[1]).abs().max()) <= 1e-3
+
+
+@pytest.mark.parametrize("fill", [0xFF, 0x7F, 0x3C])
+def test_workspaces_may_hold_anything_behind_the_header(S, fill):
+    """NaN, large numbers, valid indices: no call reads what it has not written."""
+    T, H, K = 24, 16, 300
+    step = Step(S, 10, T=T, H=H, K=K)
+    step.topk[3] = -1
+    step.topk[5, 10:] = -1
+    G = 8
+
+    def calls(ws):
+        got = []
+        for n in (0, 1, 2, 3, 5, 8):
+            got += S.sparse_mla_decode(step.q, step.kv, step.topk, SCALE, num_splits=n, ws=ws(
+                S.svt.lib().svt_sparse_mla_decode_workspace_size(T, H, K, n)))
+        got.append(S.resolve_topk_slots(step.topk, num_pages=500, ws=ws(0)))
+        enc, lens = S.build_group_union(step.topk, G, 500, ws=ws(0))
+        got.append(lens)
+        for tile in (False, True):
+            got += S.sparse_mla_prefill_grouped(step.q, G, step.kv, enc, lens, K, SCALE, union_tile=tile, ws=ws(
+                S.svt.lib().svt_sparse_mla_prefill_grouped_workspace_size(T, H, G)))
+        dq, _, w = S.sparse_mla_backward(step.q, step.kv, step.topk, SCALE, got[0], got[1], step.dout, return_weights=True,
+                                         ws=ws(S.svt.lib().svt_sparse_mla_backward_workspace_size(T, H, K, 500)))
+        return got + [dq, w]
+
+    def dirty(nbytes):
+        ws = S.Workspace(nbytes=nbytes)
+        ws.buf[256:] = fill
+        return ws
+
+    def clean(nbytes):
+        ws = S.Workspace(nbytes=nbytes)
+        ws.buf.zero_()
+        return ws
+    for a, b in zip(calls(dirty), calls(clean)):
+        assert torch.equal(a, b)
