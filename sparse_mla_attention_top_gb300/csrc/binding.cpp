@@ -241,12 +241,14 @@ PyObject* backward(PyObject* const* a) {
                       static_cast<const float*>(p_lse), p_dout, static_cast<const float*>(p_dlse), to_dq, to_dkv,
                       to_weights, ws.data_ptr(), ws_bytes, stream);
   };
-  // A call without a workspace is refused, for that or for another reason, which comes first: only a call
-  // that the library takes makes its outputs and asks for its workspace.
-  svt_status st = call(dq ? p_dq : any, dkv ? p_dkv : any, nullptr, 0);
-  if (st != SVT_ERR_WORKSPACE) return PyLong_FromLong(st);
+  svt_status st;
   const size_t need = g_backward_ws(int32(T), int32(H), int32(K), n);
-  if (ws.nbytes() < need) return PyLong_FromLongLong(-static_cast<long long>(need));
+  if (need <= 256 || n >= (1ll << 31) || ws.nbytes() < need) {  // (256: sizes that it takes for none)
+    // A call without a workspace is refused, for that or for another reason, which comes first: only a call
+    // that the library takes asks for its workspace, and the outputs are made within the sizes of one.
+    st = call(dq ? p_dq : any, dkv ? p_dkv : any, nullptr, 0);
+    return st != SVT_ERR_WORKSPACE ? PyLong_FromLong(st) : PyLong_FromLongLong(-static_cast<long long>(need));
+  }
   at::Tensor made_q, made_kv, weights;
   if (dq == nullptr) {
     made_q = at::empty({T, H, 576}, q.options());

@@ -439,7 +439,7 @@ def rope_append(latent, k_rope, positions, slots, kv: KVCache, freqs, *, layout:
     in the same launch. Returns q_out."""
     ws, capturing, _ = _workspace(ws)
     with ws.lock:
-        ws._size_to(256, capturing)
+        ws._captured |= capturing
         r = (_fast or _binding()).rope_append(latent, k_rope, positions, slots, kv.data, kv.num_pages, kv.page_size,
                                               kv.row_stride_bytes, kv.dtype, freqs, _choice(layout, ROPE_LAYOUTS, "layout"),
                                               amplitude, q_rope, q_out, ws.buf)
@@ -456,7 +456,7 @@ def sparse_mla_backward(q, kv: KVCache, topk, softmax_scale: float, out, lse, do
     (dq [T, H, 576] bf16, dkv [num_slots, 576] bf16, weights [T, K] fp32 or None)."""
     ws, capturing, _ = _workspace(ws)
     with ws.lock:
-        ws._size_to(256, capturing)
+        ws._captured |= capturing
         for _ in range(2):
             r = (_fast or _binding()).sparse_mla_backward(
                 q, kv.data, kv.num_pages, kv.page_size, kv.row_stride_bytes, kv.dtype, topk, softmax_scale, out, lse, dout,
