@@ -38,6 +38,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kPart = 16384;  // scores of one part: 64 KB as fp32
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxSplit = 8;
+constexpr int kWaitTries = 1 << 18;  // of up to 2 us each, before a wait may give up
 constexpr float kDown = 1.f / 4294967296.f;  // the e's are held times this
 constexpr float kUp = 4294967296.f;
 
@@ -327,10 +328,11 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
                   make_uint4(__float_as_uint(st.m), __float_as_uint(st.s), __float_as_uint(st.w), __float_as_uint(st.d)),
                   mapa_shared(smem_u32(&sh.arrived), tid));
     // every CTA's sums arrive here (a barrier of the cluster would also wait for the zeroes on their way
-    // to memory); should one not, the row's loss and gradient are NaN
+    // to memory); should one not, the row's loss and gradient are NaN. The time alone does not say so: it
+    // runs on while a whole cluster is switched out, whose CTAs still send to each other afterwards
     const uint64_t t0 = globaltimer();
-    while (!mbar_try_wait_cluster(smem_u32(&sh.arrived), 0)) {
-      if (globaltimer() - t0 > kWaitLimitNs) {
+    for (int tries = 0; !mbar_try_wait_cluster(smem_u32(&sh.arrived), 0); ++tries) {
+      if (tries > kWaitTries && globaltimer() - t0 > kWaitLimitNs) {
         lost = true;
         break;
       }
