@@ -423,8 +423,8 @@ SVT_API svt_status svt_sparse_mla_backward(const void* q_bf16, int32_t T, int32_
  *   loss          [T] fp32 or NULL. dscores [T, N] like scores, at dstride, or NULL; it must not
  *                 overlap scores; all N columns are written.
  * A query whose teacher values are all 0 (or which has no live entry), or whose scores are all -inf,
- * has loss 0 and gradient 0. A listed score of -inf among others gives an infinite loss; NaN inputs
- * give NaN in their own row alone. N and K at most 2^30, T at most 2^27. One kernel, no workspace.
+ * has loss 0 and gradient 0. A listed score of -inf among others gives an infinite loss, one of the
+ * type's lowest value its share of 3.4e38 / temperature; NaN inputs give NaN in their own row alone. N and K at most 2^30, T at most 2^27. One kernel, no workspace.
  */
 typedef enum { SVT_TEACHER_WEIGHTS = 0, SVT_TEACHER_LOGITS = 1 } svt_teacher_kind;
 typedef enum { SVT_DISTILL_CANDIDATES = 0, SVT_DISTILL_LISTED = 1 } svt_distill_scope;
