@@ -897,6 +897,9 @@ __device__ void softmax_role(const SharedPrefixParams& p, uint8_t* smem, uint32_
             tmem_ld16(from + 16 * h, sv);
             tmem_ld_wait();
           }
+          // (the mask behind the scale, which may be 0 or negative)
+#pragma unroll
+          for (int c = 0; c < 16; ++c) sv[c] = __float_as_uint(fmaf(__uint_as_float(sv[c]), p.scale_log2, -ref));
           if (!whole) {
 #pragma unroll
             for (int c = 0; c < 16; ++c) sv[c] = (live >> (16 * h + c)) & 1u ? sv[c] : 0xff800000u;
@@ -904,7 +907,7 @@ __device__ void softmax_role(const SharedPrefixParams& p, uint8_t* smem, uint32_
           uint32_t w[8];
 #pragma unroll
           for (int c = 0; c < 16; c += 2) {
-            const float x = fmaf(__uint_as_float(sv[c]), p.scale_log2, -ref), y = fmaf(__uint_as_float(sv[c + 1]), p.scale_log2, -ref);
+            const float x = __uint_as_float(sv[c]), y = __uint_as_float(sv[c + 1]);
             over = fmaxf(over, fmaxf(x, y));
             const float a = ex2_approx(x), z = ex2_approx(y);
             s0 += a;

@@ -377,3 +377,18 @@ def test_rows_past_32_bit_offsets():
     lists = [np.arange(150), np.r_[0:128, 192:256]]
     rows = cache.view(pages, page, 576)[at].reshape(-1, 576).double()
     R.check_attention(got, R.attention(q, rows, lists, SCALE, "bf16"))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("scale", [0.0, -SCALE, -0.5, 1e-30])
+@pytest.mark.parametrize("groups, page", [([([37, 0, 130, 1], 30), ([5], 0)], 16), ([beams(5, 129, 33)], 24),
+                                          ([beams(4, 9000, 100)], 64)], ids=["short", "rows", "cut"])
+def test_scales_of_zero_negative_and_tiny(kind, scale, groups, page):
+    """Any finite scale has its softmax (0: the mean of V). Lists that end inside tiles: what is masked stays masked."""
+    c = Case(groups, 16, page, kind, seed=27)
+    ws = S.Workspace()
+    got = S.mla_decode_shared_prefix(c.q, c.kv, c.table, c.len_t, c.start_t, c.prefix_t, scale, ws=ws)
+    assert ws.read_status() == 0
+    out, lse, d_out, d_lse = R.attention(c.q, c.rows, c.lists, scale, kind)
+    # log2 of a sum of up to 2^14 terms is off by at most two of its ulp, 2^-19, whatever the scores are
+    R.check_attention(got, (out, lse, d_out, d_lse + 2.0 ** -19))
