@@ -343,7 +343,7 @@ struct ForkParams {
   int* row_copy;   // [N] whether the row gets a copy of its parent's begun page
   int* row_first;  // [N] its first new page among the call's
   int* keeps;      // [R] whether a child keeps the row's begun page
-  int* need;       // new pages of the call
+  long long* need; // new pages of the call
   int* bad_plan;
   int* bad_rows;  // [scan_ctas]
   int scan_ctas, shares;

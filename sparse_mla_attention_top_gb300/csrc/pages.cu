@@ -18,29 +18,29 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kScanThreads = 1024;
 
-// Exclusive sums over a CTA of kN threads; *all gets the total. `part` is kN / 32 words of shared memory.
-template <int kN>
-__device__ __forceinline__ int block_scan(int v, int* part, int* all) {
+// Exclusive sums over a CTA of kN threads; *all gets the total. `part` is kN / 32 values of shared memory.
+template <int kN, typename T>
+__device__ __forceinline__ T block_scan(T v, T* part, T* all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int s = v;
+  T s = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, s, d);
+    const T o = __shfl_up_sync(0xffffffffu, s, d);
     if (lane >= d) s += o;
   }
   if (lane == 31) part[warp] = s;
   __syncthreads();
   if (warp == 0) {
-    int t = lane < kN / 32 ? part[lane] : 0;
+    T t = lane < kN / 32 ? part[lane] : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, t, d);
+      const T o = __shfl_up_sync(0xffffffffu, t, d);
       if (lane >= d) t += o;
     }
     if (lane < kN / 32) part[lane] = t;
   }
   __syncthreads();
-  const int before = warp > 0 ? part[warp - 1] : 0;
+  const T before = warp > 0 ? part[warp - 1] : 0;
   *all = part[kN / 32 - 1];
   __syncthreads();
   return before + s - v;
@@ -153,8 +153,10 @@ __device__ bool rows_are_bad(const ForkParams& p, int cta, int ctas) {
 }
 
 // For each row to come: what of its parent it keeps, and the place of its new pages among all. One CTA.
-__device__ void plan_rows(const ForkParams& p, int* part) {
+// (Their sum is in 64 bits: a row alone may ask for 2^30 pages, of which the pool need not have any.)
+__device__ void plan_rows(const ForkParams& p) {
   extern __shared__ int first[];  // [R] the first row that names a parent
+  __shared__ long long part[32];
   __shared__ int void_call;
   const int P = p.page_size;
   const long long room = static_cast<long long>(p.M_out) * P;
@@ -170,7 +172,7 @@ __device__ void plan_rows(const ForkParams& p, int* part) {
   bool bad = false;
   for (int i0 = 0; i0 < p.N; i0 += kScanThreads) {
     const int i = i0 + static_cast<int>(threadIdx.x);
-    int need = 0;
+    long long need = 0;
     if (i < p.N) {
       const int from = p.parents[i];
       const int grow = p.grow != nullptr ? p.grow[i] : p.grow_all;
@@ -190,12 +192,12 @@ __device__ void plan_rows(const ForkParams& p, int* part) {
       }
       const long long end = static_cast<long long>(len) + (bad ? 0 : grow);
       if (end > room || end > 0x7fffffffll) bad = true;
-      need = bad ? 0 : copy + static_cast<int>((end + P - 1) / P - (len + P - 1) / P);
+      need = bad ? 0 : copy + (end + P - 1) / P - (len + P - 1) / P;
       p.row_copy[i] = copy;
     }
-    int all;
-    const int s = block_scan<kScanThreads>(need, part, &all);
-    if (i < p.N) p.row_first[i] = static_cast<int>(min(base + s, 0x7fffffffll));
+    long long all;
+    const long long s = block_scan<kScanThreads>(need, part, &all);
+    if (i < p.N) p.row_first[i] = static_cast<int>(min(base + s, 0x7fffffffll));  // (more than a pool has: the call is void)
     base += all;
   }
   for (int r = threadIdx.x; r < p.R; r += kScanThreads) {
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(kScanThreads) fork_scan_kernel(const __grid_co
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ int part[32];
   if (blockIdx.x == 0) {
-    plan_rows(p, part);
+    plan_rows(p);
     return;
   }
   const int cta = blockIdx.x - 1, ctas = gridDim.x - 1;

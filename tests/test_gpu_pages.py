@@ -294,3 +294,19 @@ def test_refused_tensors():
             S.fork_pages(p.kv(p.data), i32(p.refs), i32(p.table), i32(p.lens), i32([0]), **kw)
     with pytest.raises(TypeError):
         S.compact_pages(p.kv(p.data), i32(p.refs), i32(p.table).t())
+
+
+@pytest.mark.parametrize("rows, grow", [(1024, 1 << 21), (2048, 1 << 20), (2048, 1 << 21)])
+def test_growths_beyond_32_bits_change_nothing(rows, grow):
+    # pages of one token: rows x grow of them are 2^31 (in one round of the plan's sum, and in two) and 2^32, of 70 free ones
+    free, _ = torch.cuda.mem_get_info()
+    assert free > 12 * rows * grow
+    p = Pool([(0, [16, 20])], 1, 70, seed=21)
+    refs, data, ws = i32(p.refs), p.data.clone(), S.Workspace()
+    table, lens, slots, _ = S.fork_pages(p.kv(data), refs, i32(p.table), i32(p.lens), i32([-1] * rows), grow=grow,
+                                         max_blocks=grow, ws=ws)
+    assert ws.read_status() == svt.DEV_ERR_NO_PAGES
+    assert int(table.amax()) == int(table.amin()) == -1 and int(slots.amax()) == int(slots.amin()) == -1 and not lens.any()
+    assert np.array_equal(refs.cpu().numpy(), p.refs) and torch.equal(data, p.data)
+    del table, slots
+    torch.cuda.empty_cache()
