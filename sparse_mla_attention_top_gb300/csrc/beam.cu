@@ -265,9 +265,10 @@ __device__ __forceinline__ uint64_t key_of(float x, int t) {
 
 // More candidates than the buffer holds (runs of equal logits such as a mask's, rows in ascending order): tokens [begin, end)
 // again, a step's worth at a time, against the `held` first keys of the buffer; every step's bar is its K-th key. Of a run of
-// equal logits only the first step's pass it.
+// equal logits only the first step's pass it. Returns the keys that are held then, to all threads alike (sh.count may be
+// counting the next round's by the time a thread looks).
 template <bool kF32>
-__device__ __noinline__ void select_again(const Row<kF32>& row, int begin, int end, Shared& sh, int held, int K) {
+__device__ __noinline__ int select_again(const Row<kF32>& row, int begin, int end, Shared& sh, int held, int K) {
   if (threadIdx.x == 0) sh.count = held;
   __syncthreads();
   float bar = held == K ? from_ordered(static_cast<uint32_t>(sh.buf[K - 1] >> 32)) : -__int_as_float(0x7f800000);
@@ -289,6 +290,7 @@ __device__ __noinline__ void select_again(const Row<kF32>& row, int begin, int e
     }
     held = min(n, K);
   }
+  return held;
 }
 
 // One CTA for a slice of a beam's tokens; a warp's spans come by themselves, the CTA meets at the rankings only.
@@ -386,8 +388,7 @@ __global__ void __launch_bounds__(kThreads, 3) beam_scan_kernel(const __grid_con
     const int to = r + 1 < rounds ? t_begin + (r + 1) * R::kRound : t_end;
     int got = count;
     if (count > kBuf) {
-      select_again(row, from, to, sh, held, K);
-      got = sh.count;
+      got = select_again(row, from, to, sh, held, K);
     } else if (count > held && count >= K) {
       rank_buffer(sh, count, K);
     }

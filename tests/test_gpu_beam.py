@@ -255,3 +255,20 @@ def test_refused_tensors():
         S.beam_select(logits, scores, 129)
     with pytest.raises(S.SvtError):
         S.beam_select(logits, scores, 2, finished=scores > 0, end_token=50)
+
+
+@pytest.mark.parametrize("dtype, V", [(torch.float32, 50001), (torch.bfloat16, 100001)])
+@pytest.mark.parametrize("K", [1, 100])
+def test_rounds_that_overflow_one_after_another(dtype, V, K):
+    # so many beams that each is one CTA's, over several rankings: all values of a round above those before, steps of equal
+    # ones, and both in turn; time and again, as warps run ahead of one another as they like
+    up = torch.arange(V, device="cuda", dtype=torch.float32)
+    rows = torch.stack([up * 2.0 ** -12, (up / 3000).floor(), torch.where(up % 20000 < 10000, up * 2.0 ** -12, 1.0)]).to(dtype)
+    B = 3 * torch.cuda.get_device_properties(0).multi_processor_count
+    logits = rows.repeat(B // 3, 1)[:, None]
+    scores = torch.zeros((B, 1), device="cuda")
+    want = torch.sort(rows.double(), dim=1, descending=True, stable=True).indices[:, :K].to(torch.int32).repeat(B // 3, 1)
+    first = S.beam_select(logits, scores, K)
+    assert torch.equal(first[2], want)
+    for _ in range(10):
+        assert all(torch.equal(a, b) for a, b in zip(S.beam_select(logits, scores, K), first))
