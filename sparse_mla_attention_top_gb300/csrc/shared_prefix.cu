@@ -151,12 +151,14 @@ __device__ __forceinline__ void tma2_load_2d(uint32_t dst, const void* tmap, int
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
-// Arrivals on a barrier of CTA 0 of the pair. What they announce is read by the async proxy (the MMAs' operands, behind a
-// proxy fence of the writer) or nothing at all (buffers that have been read), never by threads of the other CTA: so none
-// needs a release at cluster scope, which waits for all that the thread has in flight (a unit every 1800 cycles where
-// those were TMA loads; 2000 cycles at P).
+// Arrivals on a barrier of CTA 0 of the pair, which its MMA thread waits for at cluster scope. arrive_lead announces what the
+// warp's threads have written to their own CTA's shared memory for the MMAs (each thread behind a proxy fence, then all
+// behind a __syncwarp); its release is of that memory only. A release of everything at cluster scope waits for all that the
+// thread has in flight (128 x 64 x 32768: 459 us against 387). Relaxed arrivals hand back what has been read, or announce loads
+// whose bytes the barrier counts.
 __device__ __forceinline__ void arrive_lead(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  mbar_arrive_remote_relaxed(bar);
 }
 __device__ __forceinline__ void arrive_lead_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
@@ -169,14 +171,27 @@ __device__ __forceinline__ void tma2_load_3d(uint32_t dst, const void* tmap, int
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+// Barriers that the other CTA of the pair, or the MMAs of CTA 0, arrive on are observed at cluster scope.
+__device__ __forceinline__ bool mbar_test_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // The bounded wait of a single thread that is waited for: it looks again and again for a while before it sleeps. (A thread that
 // sleeps in a wait was seen to wake up to 1200 cycles behind the commit of MMAs that it waited for; more than a few
 // threads that look keep the others from their barriers.)
+template <bool kCluster>
 __device__ __forceinline__ bool mbar_wait_awake(uint32_t bar, uint32_t parity, const WaitCtl& wc) {
 #pragma unroll 1
   for (int i = 0; i < 256; ++i)
-    if (mbar_test_wait(bar, parity)) return true;
-  return mbar_wait<true>(bar, parity, wc);
+    if (kCluster ? mbar_test_wait_cluster(bar, parity) : mbar_test_wait(bar, parity)) return true;
+  return kCluster ? mbar_wait_cluster(bar, parity, wc) : mbar_wait<true>(bar, parity, wc);
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;
@@ -407,7 +422,7 @@ __device__ void tma_role(const SharedPrefixParams& p, uint8_t* smem, uint32_t ba
   for (uint32_t s = 0; seg.next(); ++s) {
     if (me == 0) {
       // this CTA's 64 query rows (past the row tile's end: rows that nobody stores; past q's: zeroes)
-      if (s > 0 && !mbar_wait<true>(bar(kBarQEmpty), (s - 1) & 1u, wc)) return;
+      if (s > 0 && !mbar_wait_cluster(bar(kBarQEmpty), (s - 1) & 1u, wc)) return;
       const int row = p.row_tiles[seg.row_tile].row0 + kRows * static_cast<int>(crank);
       const uint32_t on = kF16 ? bar(kBarQLand) : mapa_shared(bar(kBarQFull), 0);
       if (kF16)
@@ -421,7 +436,7 @@ __device__ void tma_role(const SharedPrefixParams& p, uint8_t* smem, uint32_t ba
     for (int t = 0; t <= nt; ++t) {
       // step t: the units of K(t), then of V(t - 1)
       const uint32_t rk = (k0 + t) % kInfos, rv = (k0 + t - 1) % kInfos;
-      if (t < nt && !mbar_wait_awake(bar(kBarInfoFull + rk), ((k0 + t) / kInfos) & 1u, wc)) return;
+      if (t < nt && !mbar_wait_awake<false>(bar(kBarInfoFull + rk), ((k0 + t) / kInfos) & 1u, wc)) return;
       const TileInfo &ik = infos[rk], &iv = infos[rv];
       const int mode_k = t < nt ? ik.mode : kFillNone, mode_v = t > 0 ? iv.mode : kFillNone;
       if (mode_k == kFillHalves && mode_v == kFillHalves && iv.fix == 0 && !withhold) {
@@ -432,7 +447,7 @@ __device__ void tma_role(const SharedPrefixParams& p, uint8_t* smem, uint32_t ba
         const int nk = 3 - turn, zv = 2 * static_cast<int>(crank) + 4 * (1 - turn);
 #pragma unroll 1
         for (int j = 0; j < nk + 2; ++j) {
-          if (!mbar_wait_awake(empty0 + 8u * at, lap ^ 1u, wc)) return;
+          if (!mbar_wait_awake<true>(empty0 + 8u * at, lap ^ 1u, wc)) return;
           const uint32_t full = lead_full + 8u * at;
           arrive_lead_expect_tx(full, kUnit);
           tma2_load_3d(ring0 + at * kUnit, &p.kv_map64, 0, j < nk ? yk : j == nk ? y0 : y1, j < nk ? 2 * turn + 4 * j : zv, full);
@@ -452,7 +467,7 @@ __device__ void tma_role(const SharedPrefixParams& p, uint8_t* smem, uint32_t ba
           const int j = v && t < nt ? i - kKUnits : i;
           const int mode = v ? mode_v : mode_k;
           const TileInfo& info = v ? iv : ik;
-          if (!mbar_wait_awake(empty0 + 8u * at, lap ^ 1u, wc)) return;
+          if (!mbar_wait_awake<true>(empty0 + 8u * at, lap ^ 1u, wc)) return;
           const uint32_t dst = ring0 + at * kUnit;
           const int* base = info.base + 4 * (v ? j >> 1 : static_cast<int>(crank));
           const int block = v ? 4 * (j & 1) + 2 * static_cast<int>(crank) : 2 * j;
@@ -701,7 +716,7 @@ __device__ void mma_role(const SharedPrefixParams& p, uint8_t* smem, uint32_t tm
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
   auto wait = [&](int i, uint32_t parity) -> bool {
-    return mbar_test_wait(bar(i), parity) || mbar_wait<true>(bar(i), parity, wc);
+    return mbar_test_wait_cluster(bar(i), parity) || mbar_wait_cluster(bar(i), parity, wc);
   };
   const uint64_t dk = smem_desc_sw128(sbase, 16, 1024), dv = smem_desc_sw128(sbase, kBlk, 1024);
   const uint32_t k_hi = static_cast<uint32_t>(dk >> 32), v_hi = static_cast<uint32_t>(dv >> 32);
@@ -852,14 +867,14 @@ __device__ void softmax_role(const SharedPrefixParams& p, uint8_t* smem, uint32_
 #pragma unroll 1
         for (int i = 0; i < kKUnits; ++i) {
           const uint32_t u = kKUnits * k + i, slot = u % kSlots;
-          mbar_wait<true>(bar(kBarSFull + slot), (u / kSlots) & 1u, wc);
+          mbar_wait_cluster(bar(kBarSFull + slot), (u / kSlots) & 1u, wc);
           tc_fence_after();
           uint32_t sv[32];
           tmem_ld32(lanes + kTmemS + 64 * slot + 32 * hs, sv);
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_lead(lead_bar(kBarSFree + slot));
+          if (lane == 0) mbar_arrive_remote_relaxed(lead_bar(kBarSFree + slot));
           if (i == kKUnits - 1) {
 #pragma unroll
             for (int c = 0; c < 32; ++c) acc[c] += __uint_as_float(sv[c]);
@@ -875,11 +890,11 @@ __device__ void softmax_role(const SharedPrefixParams& p, uint8_t* smem, uint32_
           }
         }
       } else {
-        mbar_wait<true>(bar(kBarSFull + b), (k >> 1) & 1u, wc);
+        mbar_wait_cluster(bar(kBarSFull + b), (k >> 1) & 1u, wc);
         tc_fence_after();
       }
       // the PV before the last has read this buffer of P
-      if (t > 1) mbar_wait<true>(bar(kBarPvDone + b), ((k >> 1) - 1) & 1u, wc);
+      if (t > 1) mbar_wait_cluster(bar(kBarPvDone + b), ((k >> 1) - 1) & 1u, wc);
       const uint32_t from = lanes + kTmemS + 64 * b + 32 * hs;
       uint8_t* pb = smem + kOffP + b * kPBytes + (col0 >> 6) * kBlk;
       // P relative to the reference maximum as it is; only if a score passes it by 2^8 (or is the first) it is moved and P made again
@@ -939,7 +954,7 @@ __device__ void softmax_role(const SharedPrefixParams& p, uint8_t* smem, uint32_
         l *= alpha;
         if (t > 0) {
           // O holds the tiles before this one once their PV is done
-          mbar_wait<true>(bar(kBarPvDone + (b ^ 1u)), ((k - 1) >> 1) & 1u, wc);
+          mbar_wait_cluster(bar(kBarPvDone + (b ^ 1u)), ((k - 1) >> 1) & 1u, wc);
           tc_fence_after();
           if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
@@ -959,7 +974,7 @@ __device__ void softmax_role(const SharedPrefixParams& p, uint8_t* smem, uint32_
       l += sum;
       tc_fence_before();
       __syncwarp();
-      if (!kF16 && lane == 0) arrive_lead(lead_bar(kBarSFree + b));
+      if (!kF16 && lane == 0) mbar_arrive_remote_relaxed(lead_bar(kBarSFree + b));
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
@@ -972,7 +987,7 @@ __device__ void softmax_role(const SharedPrefixParams& p, uint8_t* smem, uint32_
 #pragma unroll
     for (int i = 0; i < 4; ++i) total += sums[i * kRows + row];
     named_bar_sync(named, 128);  // (sums is written again by the next segment)
-    mbar_wait<true>(bar(kBarPvDone + ((k - 1) & 1u)), ((k - 1) >> 1) & 1u, wc);
+    mbar_wait_cluster(bar(kBarPvDone + ((k - 1) & 1u)), ((k - 1) >> 1) & 1u, wc);
     tc_fence_after();
     const float inv = total > 0.f ? 1.f / total : (total == total ? 0.f : total);
     const float lse2 = total > 0.f ? m + __log2f(total) : (total == total ? -CUDART_INF_F : total);

@@ -392,3 +392,13 @@ def test_scales_of_zero_negative_and_tiny(kind, scale, groups, page):
     out, lse, d_out, d_lse = R.attention(c.q, c.rows, c.lists, scale, kind)
     # log2 of a sum of up to 2^14 terms is off by at most two of its ulp, 2^-19, whatever the scores are
     R.check_attention(got, (out, lse, d_out, d_lse + 2.0 ** -19))
+
+
+@pytest.mark.parametrize("kind, page", [("bf16", 64), ("bf16", 24), ("e4m3", 64)])
+def test_outputs_repeat_to_the_bit(kind, page):
+    # units by TMA, by TMA with zeroes put in, and by threads; P and units of both CTAs of a pair are read by the MMAs of one
+    c = Case([beams(30, 1500, 300), beams(9, 700, 33)], 64, page, kind, seed=28)
+    out, lse = c.check()
+    for _ in range(30):
+        again = c.run()
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
