@@ -1116,8 +1116,9 @@ __global__ void __launch_bounds__(block_threads(kF16), 1) shared_prefix_kernel(c
     if (elect_one()) tma_role<kF16>(p, smem, bars, crank, warp == kTmaWarp0 ? 0 : 1, wc);
   }
   __syncwarp();
-  // no MMA may still read shared memory or write TMEM when the CTAs let go of them
-  if (threadIdx.x == 0) mbar_wait_ignoring_abort(bars + 8u * kBarDrain, 0, wc);
+  // No MMA may still read shared memory or write TMEM when the CTAs let go of them. (A softmax thread waits, whose role ends with
+  // the MMAs: the limit of a wait is not one of the kernel's whole time.)
+  if (threadIdx.x == 32 * kSoftWarp0) mbar_wait_ignoring_abort(bars + 8u * kBarDrain, 0, wc);
   __syncwarp();
   tc_fence_before();
   cluster_sync_all();

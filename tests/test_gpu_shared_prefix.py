@@ -402,3 +402,31 @@ def test_outputs_repeat_to_the_bit(kind, page):
     for _ in range(30):
         again = c.run()
         assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
+def test_a_call_may_take_longer_than_one_wait():
+    # some 9 ms of tiles, where a wait gives up after 2
+    pages, page, H, T, n = 6250, 64, 128, 128, 400_000
+    g = torch.Generator(device=dev())
+    g.manual_seed(29)
+    kv = S.KVCache(make_cache(g, pages * page, "bf16"), pages, page, S.KV_BF16)
+    q = torch.randn((T, H, 576), generator=g, device=dev()).to(torch.bfloat16)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=dev())  # noqa: E731
+    table = torch.arange(pages, dtype=torch.int32, device=dev())[None]
+    call = lambda: S.mla_decode_shared_prefix(q, kv, table, i32([n] * T), i32([0, T]), i32([n]), SCALE,  # noqa: E731
+                                              req_of_token=i32([0] * T), ws=ws)
+    ws = S.Workspace()
+    want = call()
+    torch.cuda.synchronize()
+    S.debug_pipeline_fault(0, 2_000_000)
+    try:
+        begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        begin.record()
+        got = call()
+        end.record()
+        torch.cuda.synchronize()
+    finally:
+        S.debug_pipeline_fault(0, 0)
+    assert begin.elapsed_time(end) > 4
+    assert ws.read_status() == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
