@@ -419,7 +419,8 @@ __device__ void tma_role(const SharedPrefixParams& p, uint8_t* smem, uint32_t ba
   const uint32_t empty0 = bar(kBarEmpty);
   uint32_t k0 = 0;
   bool withhold = (p.fault & kFaultWithholdFirstFill) != 0;
-  for (uint32_t s = 0; seg.next(); ++s) {
+  uint32_t s = 0;
+  for (; seg.next(); ++s) {
     if (me == 0) {
       // this CTA's 64 query rows (past the row tile's end: rows that nobody stores; past q's: zeroes)
       if (s > 0 && !mbar_wait_cluster(bar(kBarQEmpty), (s - 1) & 1u, wc)) return;
@@ -509,6 +510,7 @@ __device__ void tma_role(const SharedPrefixParams& p, uint8_t* smem, uint32_t ba
     }
     k0 += nt;
   }
+  if (me == 0 && s > 0) mbar_wait_cluster(bar(kBarQEmpty), (s - 1) & 1u, wc);  // (the last one lands before the CTA leaves)
 }
 
 // The fill warps fill the units that are granted to them: 16-byte pieces of 64 rows, zeroes where there is no row; or put the zeroes
@@ -1056,6 +1058,23 @@ __device__ void softmax_role(const SharedPrefixParams& p, uint8_t* smem, uint32_
   }
 }
 
+// One thread of each CTA, behind the roles' last use of the MMAs: waits until they are done and each of their arrivals on this
+// CTA's barriers has landed, the last ones too, which no role needs. (What a parity cannot tell, that the phase before a
+// barrier's last is over, is known: the last one's unit or P was made behind a wait for it or for MMAs issued later.)
+__device__ void drain(const SharedPrefixParams& p, uint32_t bars, const WaitCtl& wc) {
+  auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
+  if (!mbar_wait_ignoring_abort(bar(kBarDrain), 0, wc)) return;
+  const PairStart s = p.pairs[blockIdx.x >> 1];
+  const long long tiles = s.hi - s.lo;
+  auto last = [&](int i, long long phases) {
+    if (phases > 0) mbar_wait_cluster(bar(i), static_cast<uint32_t>(phases - 1) & 1u, wc);
+  };
+#pragma unroll 1
+  for (int i = 0; i < kUnits; ++i) last(kBarEmpty + i, ((kKUnits + kVUnits) * tiles - i + kUnits - 1) / kUnits);
+  last(kBarPvDone, (tiles + 1) / 2);
+  last(kBarPvDone + 1, tiles / 2);
+}
+
 template <bool kF16>
 __global__ void __launch_bounds__(block_threads(kF16), 1) shared_prefix_kernel(const __grid_constant__ SharedPrefixParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -1116,19 +1135,18 @@ __global__ void __launch_bounds__(block_threads(kF16), 1) shared_prefix_kernel(c
     if (elect_one()) tma_role<kF16>(p, smem, bars, crank, warp == kTmaWarp0 ? 0 : 1, wc);
   }
   __syncwarp();
-  // No MMA may still read shared memory or write TMEM when the CTAs let go of them. (A softmax thread waits, whose role ends with
-  // the MMAs: the limit of a wait is not one of the kernel's whole time.)
-  if (threadIdx.x == 32 * kSoftWarp0) mbar_wait_ignoring_abort(bars + 8u * kBarDrain, 0, wc);
+  // No MMA may still read shared memory or write TMEM when the CTAs let go of them, and nothing may be on its way to a CTA that has
+  // left: the MMAs' arrivals are waited for here, loads were by the MMAs, and the threads' own arrivals are behind the cluster's
+  // barrier. (A softmax thread waits, whose role ends with the MMAs: the limit of a wait is not one of the kernel's whole time.)
+  if (threadIdx.x == 32 * kSoftWarp0) drain(p, bars, wc);
   __syncwarp();
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
-  if (threadIdx.x == 0) {
-    // arrivals that nobody waits for (and, after a wait that gave up, loads and messages on their way) land before either
-    // CTA leaves
-    const uint64_t hold_ns = *abort_flag ? 50000u : 1000u;
+  if (threadIdx.x == 0 && *abort_flag) {
+    // after a wait that gave up, loads and arrivals that nobody waited for land first
     const uint64_t t0 = globaltimer();
-    for (int i = 0; i < 4096 && globaltimer() - t0 < hold_ns; ++i) __nanosleep(64);
+    for (int i = 0; i < 4096 && globaltimer() - t0 < 50000u; ++i) __nanosleep(64);
   }
   __syncwarp();
   cluster_sync_all();

@@ -430,3 +430,31 @@ def test_a_call_may_take_longer_than_one_wait():
     assert begin.elapsed_time(end) > 4
     assert ws.read_status() == 0
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_no_wait_runs_out_whatever_the_number_of_tiles(kind):
+    # a kernel leaves when the last arrival on each of its barriers has landed: as many as its tiles make, 0 to 9 a CTA pair
+    page = 64
+    pages = 2 * (76 * 9 + 1)
+    g = torch.Generator(device=dev())
+    g.manual_seed(30)
+    cache = make_cache(g, pages * page, kind)
+    kv = S.KVCache(cache, pages, page, S.KV_BF16 if kind == "bf16" else S.KV_FP8_E4M3)
+    rows = R.cache_rows(cache, kind)
+    q = torch.randn((4, 16, 576), generator=g, device=dev()).to(torch.bfloat16)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=dev())  # noqa: E731
+    table = torch.arange(pages, dtype=torch.int32, device=dev())[None]
+    scores = q.flatten(0, 1).double() @ rows.T * SCALE
+    ws = S.Workspace()
+    S.debug_pipeline_fault(0, 100_000_000)
+    try:
+        for tiles in [1, 2, 3, 7, 75, 76, 77] + [76 * m + r for m in range(1, 10) for r in (0, 1, 38)][2:-2]:
+            n = 128 * tiles - 5
+            _, lse = S.mla_decode_shared_prefix(q, kv, table, i32([n] * 4), i32([0, 4]), i32([n]), SCALE,
+                                                req_of_token=i32([0] * 4), ws=ws)
+            assert ws.read_status() == 0, tiles
+            bound = 1.2e-3 if kind == "bf16" else 2.5e-2  # (576 2^-23 and 2^-10 of sums of magnitudes of some 20)
+            assert float((lse.flatten().double() - scores[:, :n].logsumexp(1)).abs().amax()) < bound, tiles
+    finally:
+        S.debug_pipeline_fault(0, 0)
