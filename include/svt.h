@@ -451,7 +451,8 @@ SVT_API svt_status svt_distill_topk(const void* scores, svt_dtype dtype, int32_t
  *                 - 1. A query of no group is not computed: its rows of out and lse are left as they were.
  *   prefix_lens   [num_groups] int32: positions below prefix_lens[g] have the same content for all queries of the group
  *                 and are read through the block table of the group's first query (whose row must reach as far as any of
- *                 the group's queries attends below prefix_lens[g]). 0: nothing is shared. It may be longer than the queries:
+ *                 the group's queries attends below prefix_lens[g]; where its request id is out of range, through the row of
+ *                 the longest query that is computed together with the one at hand). 0: nothing is shared. It may be longer than the queries:
  *                 each keeps to its own length, so that the new tokens of one request are a group whose prefix is all of it.
  *                 group_start or prefix_lens out of range set SVT_DEV_ERR_INDEX_RANGE; groups are then cut or empty.
  *   out_bf16      [T, H, 512] bf16; lse [T, H] fp32 or NULL.

@@ -1283,18 +1283,19 @@ __global__ void __launch_bounds__(kPlanThreads) shared_prefix_plan_kernel(const 
       rt.t_last = begin + static_cast<int>((first + rt.nrows - 1) / p.H);
       rt.prefix_len = prefix_of(a);
       rt.min_len = 0x7fffffff;
-      int most = 0;
+      int most = 0, longest = begin;
       for (int t = rt.t_first; t <= rt.t_last; ++t) {
         const int len = near ? near_len[t] : p.token_len[t];
         rt.min_len = min(rt.min_len, len);
-        most = max(most, len);
+        if (len > most) most = len, longest = t;
       }
       rt.shared_len = min(rt.prefix_len, most);
       rt.shared_pieces = (rt.shared_len + kListPiece - 1) / kListPiece;
-      // (the prefix is read through the group's first query's table)
-      const int req = p.req_of_token != nullptr ? p.req_of_token[begin] : begin;
-      rt.req = req >= 0 && req < p.num_reqs ? req : 0;
-      if (rt.req != req) rt.shared_len = rt.shared_pieces = 0;
+      // The prefix is read through the group's first query's table; if that one has no request, through that of the row
+      // tile's longest query (which has one, unless all are empty).
+      auto request = [&](int t) { return p.req_of_token != nullptr ? p.req_of_token[t] : t; };
+      rt.req = request(begin);
+      if (rt.req < 0 || rt.req >= p.num_reqs) rt.req = most > 0 ? request(longest) : 0;
       p.row_tiles[r] = rt;
       const long long own = near ? near_before[rt.t_last + 1] - near_before[rt.t_first]
                                  : p.own_before[rt.t_last + 1] - p.own_before[rt.t_first];

@@ -458,3 +458,24 @@ def test_no_wait_runs_out_whatever_the_number_of_tiles(kind):
             assert float((lse.flatten().double() - scores[:, :n].logsumexp(1)).abs().amax()) < bound, tiles
     finally:
         S.debug_pipeline_fault(0, 0)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("bad", [-1, 99])
+def test_a_group_whose_first_request_is_out_of_range(kind, bad):
+    # only the first query is without rows: the others keep the prefix, in each of the group's row tiles
+    c = Case([beams(9, 700, 60), ([200, 3, 0, 150], 160), beams(2, 90, 9)], 64, 16, kind, seed=31)
+    first = [0, 9]
+    req = torch.arange(c.T, dtype=torch.int32, device=dev())
+    req[first] = bad
+    ws = S.Workspace()
+    got = c.run(ws, req_of_token=req)
+    assert ws.read_status() == svt.DEV_ERR_INDEX_RANGE
+    assert not got[0][first].any() and torch.isneginf(got[1][first]).all()
+    R.check_attention(got, c.want(), [t for t in range(c.T) if t not in first])
+    # a group of which nobody has a request
+    req[9:13] = bad
+    got = c.run(ws, req_of_token=req)
+    assert ws.read_status() == svt.DEV_ERR_INDEX_RANGE
+    assert not got[0][9:13].any() and torch.isneginf(got[1][9:13]).all()
+    R.check_attention(got, c.want(), list(range(1, 9)) + [13, 14])
