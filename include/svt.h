@@ -482,7 +482,8 @@ SVT_API svt_status svt_mla_decode_shared_prefix(const void* q_bf16, int32_t T, i
  *   finished      [B, W] bytes or NULL: a beam marked non-zero has one candidate, end_token with value scores[w]; its
  *                 logits are not read.
  *   out_scores, parents, tokens  [B, K] fp32 and int32: value, beam (0 .. W - 1) and token. Where there are fewer than K
- *                 candidates: -inf, -1, -1.
+ *                 candidates: -inf, -1, -1 (a caller that makes rows of a table of parents, b * W + parent, keeps -1 as it is: for
+ *                 svt_fork_pages an empty row).
  * Values are compared in fp64 (with normalisers summed from fp32 exponentials, about 1e-7 off) and rounded to fp32 once.
  * W and K at most 128, W * K at most 8192, W * V below 2^31. Two kernels.
  * Workspace: svt_beam_select_workspace_size(B, W, V, K), which depends on the current device's SM count.

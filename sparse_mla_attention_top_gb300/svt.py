@@ -531,7 +531,8 @@ def mla_decode_shared_prefix(q, kv: KVCache, block_table, lens, group_start, pre
 def beam_select(logits, scores, K: int, *, finished=None, end_token: int = 0, ws: Optional[Workspace] = None):
     """svt_beam_select: the K best continuations of each batch item's beams. logits [B, W, V] fp32 or bf16 (unit column
     stride), scores [B, W] fp32, finished [B, W] bool or uint8. Returns (scores [B, K] fp32, parents [B, K] int32, tokens
-    [B, K] int32) in descending order, (-inf, -1, -1) where there are fewer."""
+    [B, K] int32) in descending order, (-inf, -1, -1) where there are fewer: a parent of -1 stays -1 where parents become
+    rows of a table for fork_pages (b * W - 1 is another item's)."""
     return _with_workspace(ws, "svt_beam_select", lambda buf: (_fast or _binding()).beam_select(
         logits, scores, K, finished, end_token, buf))
 

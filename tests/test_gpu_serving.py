@@ -71,3 +71,44 @@ def test_steps_of_a_search(kind):
     # the search ends: every page is free
     S.fork_pages(kv, refs, table, lens, i32([]), ws=ws)
     assert not refs.any()
+
+
+def test_items_with_fewer_candidates_than_beams():
+    """Items in the middle of the batch that run out of candidates: their rows come back empty, and no other item's row goes on
+    in their place."""
+    B, W, V, H, page, pages, blocks = 4, 4, 300, 16, 16, 200, 8
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    kv = S.KVCache(torch.randn((pages * page, 576), generator=g, device="cuda").to(torch.bfloat16).view(torch.uint8), pages,
+                   page, S.KV_BF16)
+    refs, ws = torch.zeros(pages, dtype=torch.int32, device="cuda"), S.Workspace()
+    empty = torch.empty((0, blocks), dtype=torch.int32, device="cuda")
+    prompt = [40, 33, 64, 17]
+    table, lens, _, _ = S.fork_pages(kv, refs, empty, empty[:, 0], i32([-1] * B), grow=i32(prompt), max_grow=max(prompt), ws=ws)
+    table, lens, _, _ = S.fork_pages(kv, refs, table, lens, i32(np.repeat(np.arange(B), W)), ws=ws)
+    logits = torch.randn((B, W, V), generator=g, device="cuda")
+    logits[1, :, 2:] = -torch.inf  # two tokens left in one beam of item 1, none in the others
+    logits[1, 1:] = -torch.inf
+    logits[2] = float("nan")       # no candidate in item 2
+    value, parents, tokens = S.beam_select(logits, torch.zeros((B, W), device="cuda"), W, ws=ws)
+    assert parents[1].tolist()[2:] == [-1, -1] and parents[1].tolist()[:2] == [0, 0] and (parents[2] == -1).all()
+    first = torch.arange(B, dtype=torch.int32, device="cuda")[:, None] * W
+    rows = torch.where(parents >= 0, parents + first, -1).flatten()
+    old = table.clone()
+    table, lens, slots, _ = S.fork_pages(kv, refs, table, lens, rows, grow=1, ws=ws)
+    assert ws.read_status() == 0
+    live = (parents >= 0).flatten().tolist()
+    for i, go_on in enumerate(live):
+        assert int(lens[i]) == (prompt[i // W] + 1 if go_on else 1)
+        full = prompt[i // W] // page if go_on else 0
+        assert torch.equal(table[i, :full], old[i // W * W, :full])
+    assert int(refs.sum()) == int((table >= 0).sum())
+    held = R.cache_rows(kv.data, "bf16")
+    q = torch.randn((B * W, H, 576), generator=g, device="cuda").to(torch.bfloat16)
+    got = S.mla_decode_shared_prefix(q, kv, table, lens, i32(np.arange(B + 1) * W), i32(prompt), 576 ** -0.5, ws=ws)
+    assert ws.read_status() == 0
+    # (an empty row's one position lies below its group's prefix and is read through the group's first row)
+    at = lambda i, n: [int(table[i, p // page]) * page + p % page for p in range(n)]  # noqa: E731
+    lists = [np.asarray(at(i, int(lens[i])) if go_on else at(i // W * W, 1)) for i, go_on in enumerate(live)]
+    R.check_attention(got, R.attention(q, held, lists, 576 ** -0.5, "bf16"))

@@ -100,3 +100,35 @@ def test_a_pool_of_any_size_has_a_workspace_of_a_quarter_byte_a_page(L):
     for pages in (1, 33, 1024, 1025, 524288, 524289, 10_000_019, (1 << 31) - 1):
         n = L.svt_compact_pages_workspace_size(pages)
         assert pages / 4 <= n <= pages / 4 + 4096, pages
+
+
+def test_the_documented_search_step_leaves_missing_candidates_without_a_parent():
+    """The example of a search step, run up to its fork: an item with fewer candidates than beams names no other item's row."""
+    import pathlib
+    from unittest import mock
+
+    import torch
+
+    text = pathlib.Path(__file__).resolve().parents[1].joinpath("README.md").read_text()
+    block = next(b for b in text.split("```python")[1:] if "S.beam_select" in b).split("```")[0]
+    seen = {}
+
+    class Names(dict):
+        def __missing__(self, name):
+            return mock.MagicMock()
+
+    B, W = 3, 4
+    parents = torch.tensor([[3, 0, 0, 1], [2, 2, -1, -1], [-1, -1, -1, -1]], dtype=torch.int32)
+    S = mock.MagicMock()
+    S.beam_select.return_value = (torch.zeros(B, W), parents, torch.zeros(B, W, dtype=torch.int32))
+
+    def fork(kv, refs, bt, seq, rows, **kw):
+        seen["rows"] = rows
+        return (mock.MagicMock(),) * 4
+
+    S.fork_pages.side_effect = fork
+    S.mla_decode_shared_prefix.return_value = (None, None)
+    S.compact_pages.return_value = (None, None, None)
+    exec(compile(block, "README.md", "exec"), {}, Names(S=S, torch=torch, B=B, W=W))
+    assert seen["rows"].dtype == torch.int32
+    assert seen["rows"].tolist() == [3, 0, 0, 1, 6, 6, -1, -1, -1, -1, -1, -1]
