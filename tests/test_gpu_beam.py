@@ -272,3 +272,14 @@ def test_rounds_that_overflow_one_after_another(dtype, V, K):
     assert torch.equal(first[2], want)
     for _ in range(10):
         assert all(torch.equal(a, b) for a, b in zip(S.beam_select(logits, scores, K), first))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B, V", [(64, 50257), (600, 32003), (512, 131072)])
+def test_normalisers(dtype, B, V):
+    # rows cut in slices and rows of one CTA; scores that leave the values near 0, where their own rounding is none
+    logits, _ = draw(B, 1, V, dtype, 17)
+    x = logits.double()
+    scores = (x.logsumexp(2) - x.amax(2)).float()
+    value, _, _ = S.beam_select(logits, scores, 1)
+    assert R.normaliser_error(value, logits, scores) < R.NORMALISER

@@ -479,3 +479,21 @@ def test_a_group_whose_first_request_is_out_of_range(kind, bad):
     assert ws.read_status() == svt.DEV_ERR_INDEX_RANGE
     assert not got[0][9:13].any() and torch.isneginf(got[1][9:13]).all()
     R.check_attention(got, c.want(), list(range(1, 9)) + [13, 14])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("groups, page", [([([1, 2, 9, 10, 17], 1)], 16), ([beams(7, 500, 300), beams(3, 33, 5)], 16),
+                                          ([beams(5, 129, 33)], 24), ([beams(24, 3000, 100)], 64)],
+                         ids=["few", "own", "rows", "cut"])
+def test_lse_of_scores_without_rounding(kind, groups, page):
+    # whole numbers: the scores' sums are exact, and what is left is a hundred-thousandth. A row too many or too few, or codes
+    # times scales rounded to f16, is more (tests/test_serving_bounds.py)
+    scale = 2.0 ** -8
+    c = Case(groups, 16, page, kind, seed=32)
+    c.q, cache = R.whole_numbers(c.q, c.cache, kind)
+    c.cache.copy_(cache)
+    ws = S.Workspace()
+    _, lse = S.mla_decode_shared_prefix(c.q, c.kv, c.table, c.len_t, c.start_t, c.prefix_t, scale, ws=ws)
+    assert ws.read_status() == 0
+    want, bound = R.lse_of_whole_numbers(c.q, R.cache_rows(c.cache, kind), c.lists, scale, kind)
+    assert bool(((lse.double() - want).abs() <= bound).all()), float(((lse.double() - want).abs() / bound).max())
