@@ -460,9 +460,10 @@ SVT_API svt_status svt_distill_topk(const void* scores, svt_dtype dtype, int32_t
  * reach the other queries of that row tile; rows that none of them attends to are never read.
  * P is rounded to bf16 once; every sum is fp32. With an e4m3 cache P, q, the rope columns and V (code times scale) are f16 (a
  * value beyond its range sets SVT_DEV_ERR_FP8_RANGE), scores are of the codes themselves with their scales in fp32. The parts of
- * rows that are computed in two or more are f16 times a power of two for each 128 channels. T * H below 2^30, max_blocks * page_size at most
- * 2^30, num_groups at most 2^24. Three kernels. Workspace: svt_mla_decode_shared_prefix_workspace_size(T, H, num_groups),
- * which depends on the current device (about 20 MB, for the row tiles that two CTA pairs share, and some 60 bytes a query).
+ * rows that are computed in two or more are f16 times a power of two for each 128 channels. T * H below 2^30,
+ * max_blocks * page_size at most 2^30 (with fewer than 5 heads also below 2^35 / the queries that share 128 rows),
+ * num_groups at most 2^24. Three kernels. Workspace: svt_mla_decode_shared_prefix_workspace_size(T, H, num_groups), which
+ * depends on the current device (about 20 MB, for the row tiles that two CTA pairs share, and some 60 bytes a query).
  */
 SVT_API size_t svt_mla_decode_shared_prefix_workspace_size(int32_t T, int32_t H, int32_t num_groups);
 SVT_API svt_status svt_mla_decode_shared_prefix(const void* q_bf16, int32_t T, int32_t H, const svt_kv_cache* kv,
@@ -482,8 +483,8 @@ SVT_API svt_status svt_mla_decode_shared_prefix(const void* q_bf16, int32_t T, i
  *   finished      [B, W] bytes or NULL: a beam marked non-zero has one candidate, end_token with value scores[w]; its
  *                 logits are not read.
  *   out_scores, parents, tokens  [B, K] fp32 and int32: value, beam (0 .. W - 1) and token. Where there are fewer than K
- *                 candidates: -inf, -1, -1 (a caller that makes rows of a table of parents, b * W + parent, keeps -1 as it is: for
- *                 svt_fork_pages an empty row).
+ *                 candidates: -inf, -1, -1 (a caller that makes rows of a table of parents, b * W + parent, keeps -1 as it
+ *                 is: for svt_fork_pages an empty row).
  * Values are compared in fp64 (with normalisers summed from fp32 exponentials, about 1e-7 off) and rounded to fp32 once.
  * W and K at most 128, W * K at most 8192, W * V below 2^31. Two kernels.
  * Workspace: svt_beam_select_workspace_size(B, W, V, K), which depends on the current device's SM count.

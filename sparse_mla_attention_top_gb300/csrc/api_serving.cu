@@ -151,6 +151,10 @@ svt_status svt_mla_decode_shared_prefix(const void* q_bf16, int32_t T, int32_t H
       return set_last_error(SVT_ERR_INVALID_ARG, "block_table must not be null, num_reqs and max_blocks must be > 0");
     if (max_blocks * static_cast<long long>(kv->page_size) > kMaxTokens)
       return set_last_error(SVT_ERR_UNSUPPORTED, "max_blocks * page_size must be at most 2^30");
+    // the pieces of a row tile, its queries' own and the prefix's, are counted in 32 bits
+    const long long pieces = max_blocks * static_cast<long long>(kv->page_size) / svt::kListPiece + 2;
+    if ((std::min(T, (126 + H) / H + 1) + 1) * pieces >= (1ll << 31) - 8)
+      return set_last_error(SVT_ERR_UNSUPPORTED, "the tables of the queries of 128 rows must have fewer than 2^35 positions");
     if (req_of_token == nullptr && num_reqs < T)
       return set_last_error(SVT_ERR_INVALID_ARG, "without req_of_token every query needs a row of block_table");
     if (q_bf16 == nullptr || out_bf16 == nullptr || lens == nullptr || group_start == nullptr || prefix_lens == nullptr)

@@ -132,3 +132,16 @@ def test_the_documented_search_step_leaves_missing_candidates_without_a_parent()
     exec(compile(block, "README.md", "exec"), {}, Names(S=S, torch=torch, B=B, W=W))
     assert seen["rows"].dtype == torch.int32
     assert seen["rows"].tolist() == [3, 0, 0, 1, 6, 6, -1, -1, -1, -1, -1, -1]
+
+
+def test_shared_prefix_lists_beyond_32_bits_are_refused(L):
+    # a row tile of 128 (query, head) rows counts its list in pieces of 16 positions: H = 1 has 128 queries in one
+    def call(T, H, mb, page=64):
+        kv = _kv(page_size=page)
+        return L.svt_mla_decode_shared_prefix(A, T, H, ctypes.byref(kv), A, T, mb, None, A, A, A, 2, ctypes.c_float(0.04),
+                                              OUT, None, WS, 300, None)
+    most = (1 << 30) // 64
+    assert call(128, 1, most) == UNS and "2^35" in L.svt_last_error_string().decode()
+    assert call(31, 1, most) == UNS and call(30, 1, most) == SMALL
+    assert call(4096, 4, most) == UNS and call(4096, 5, most) == SMALL and call(4096, 128, most) == SMALL
+    assert call(128, 1, most // 8) == SMALL and call(128, 1, (1 << 30) // 7, page=7) == UNS
