@@ -183,13 +183,14 @@ svt_status svt_mla_decode_shared_prefix(const void* q_bf16, int32_t T, int32_t H
   p.num_reqs = num_reqs;
   p.max_blocks = max_blocks;
   p.page_size = kv->page_size;
-  // (of two for a tile of the prefix. bf16, measured for shares by 1, 1.5 and 2 tiles: 64 x 64 x 8192 69, 67 and 67 us, 128 x 64 x
-  // 32768 383, 382 and 388. Threads load all tiles of an e4m3 cache: 5 x 24 x 16 x 12007 99 us, 110 with 2 tiles)
-  p.own_cost = kv->dtype == SVT_KV_BF16 ? 3 : 2;
+  p.pieces = kv->dtype == SVT_KV_BF16 && kv->page_size % svt::kListPiece == 0;
+  // (of two for a tile of the prefix. Own rows by TMA in pieces, measured for shares by 1, 1.5 and 2 tiles: 64 x 64 x 8192 69, 67
+  // and 67 us, 128 x 64 x 32768 383, 382 and 388. Where threads load all tiles, these cost alike: an e4m3 cache 5 x 24 x 16 x 12007
+  // 99 us (by 2: 110), bf16 with pages of 24 rows 64 x 64 x 8192 228 us (by 1.5: 237), 5 x 24 x 16 x 12007 124 (130))
+  p.own_cost = p.pieces ? 3 : 2;
   p.page_shift = -1;
   for (int i = 0; i < 31; ++i)
     if (kv->page_size == 1 << i) p.page_shift = i;
-  p.pieces = kv->dtype == SVT_KV_BF16 && kv->page_size % svt::kListPiece == 0;
   p.row_bytes = kv->dtype == SVT_KV_BF16 ? svt::kRowBytesBf16 : svt::kRowBytesFp8;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.out = static_cast<uint16_t*>(out_bf16);

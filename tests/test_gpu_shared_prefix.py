@@ -497,3 +497,8 @@ def test_lse_of_scores_without_rounding(kind, groups, page):
     assert ws.read_status() == 0
     want, bound = R.lse_of_whole_numbers(c.q, R.cache_rows(c.cache, kind), c.lists, scale, kind)
     assert bool(((lse.double() - want).abs() <= bound).all()), float(((lse.double() - want).abs() / bound).max())
+
+
+def test_more_tiles_than_a_few_a_pair_in_pages_of_24_rows():
+    # loaded by threads, whose tiles cost the same whether rows are shared or not
+    Case([beams(7, 5000, 900), ([4000], 0), beams(9, 100, 900), ([], 5), ([0], 3), ([6000] * 4, 6000)], 128, 24, seed=33).check()
