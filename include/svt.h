@@ -457,7 +457,7 @@ SVT_API svt_status svt_distill_topk(const void* scores, svt_dtype dtype, int32_t
  *                 group_start or prefix_lens out of range set SVT_DEV_ERR_INDEX_RANGE; groups are then cut or empty.
  *   out_bf16      [T, H, 512] bf16; lse [T, H] fp32 or NULL.
  * A value that is not finite in a cache row that some query of a row tile (128 consecutive rows of a group) attends to can
- * reach the other queries of that row tile; rows that none of them attends to are never read.
+ * reach the other queries of that row tile; rows that none of them attends to have no effect.
  * P is rounded to bf16 once; every sum is fp32. With an e4m3 cache P, q, the rope columns and V (code times scale) are f16 (a
  * value beyond its range sets SVT_DEV_ERR_FP8_RANGE), scores are of the codes themselves with their scales in fp32. The parts of
  * rows that are computed in two or more are f16 times a power of two for each 128 channels. T * H below 2^30,
@@ -485,7 +485,8 @@ SVT_API svt_status svt_mla_decode_shared_prefix(const void* q_bf16, int32_t T, i
  *   out_scores, parents, tokens  [B, K] fp32 and int32: value, beam (0 .. W - 1) and token. Where there are fewer than K
  *                 candidates: -inf, -1, -1 (a caller that makes rows of a table of parents, b * W + parent, keeps -1 as it
  *                 is: for svt_fork_pages an empty row).
- * Values are compared in fp64 (with normalisers summed from fp32 exponentials, about 1e-7 off) and rounded to fp32 once.
+ * Values are compared in fp64 (with normalisers summed from fp32 exponentials, about 1e-7 off) and rounded to fp32 once. The K
+ * candidates that a beam can have are those of its largest logits, also where a score is so large that their values are equal.
  * W and K at most 128, W * K at most 8192, W * V below 2^31. Two kernels.
  * Workspace: svt_beam_select_workspace_size(B, W, V, K), which depends on the current device's SM count.
  */

@@ -23,7 +23,7 @@
 // blocks of 128 channels have a scale each, so that each K unit's sums go to one of four slots of 64 TMEM columns, from which the
 // softmax warps collect them, times their scales, in fp32.
 //
-// What bounds it: bf16, 128 queries x 64 heads over 32768 rows: 382 us, 1.55 PFLOP/s (a step of the loop is 2200 to 2450 cycles, the
+// What bounds it: bf16, 128 queries x 64 heads over 32768 rows: 382 to 390 us, 1.55 PFLOP/s (a step of the loop is 2200 to 2450 cycles, the
 // MMAs of a tile alone 2180; the rest is power and the last pairs' tails); 64 x 64 x 8192: 67 us, of which the plan and the merge are
 // some 12. e4m3, 120 x 16 x 12007: 100 us, 9000 cycles a tile: a warp takes some 6000 to load and convert a unit, and the
 // softmax warps as long for five units of scores and their P.
